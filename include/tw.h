@@ -8,9 +8,10 @@
  *   [G] "TokenWeave Guide: Compute-Communication Overlap for LLMs"
  *
  * Conventions shared by every call:
- *   - Tensors are bf16, row-major and contiguous: a [T, H] tensor is T token
- *     rows of H hidden values, row stride H elements. A shard or half of a
- *     tensor is passed by offsetting its pointers by row0 * H elements.
+ *   - Tensors are row-major and contiguous: a [T, H] tensor is T token rows of
+ *     H hidden values, row stride H elements, bf16 where a call does not say
+ *     otherwise. A shard or half of a tensor is passed by offsetting its
+ *     pointers by row0 * H elements.
  *   - The caller owns every buffer. libtw allocates no device memory; it keeps
  *     only per-device launch attributes (SM count, shared-memory limit, L2
  *     size, which sets the per-call L2 policy).
@@ -55,12 +56,17 @@ typedef struct CUevent_st* tw_event_t; /* == cudaEvent_t */
 #define TW_MAX_PARTIALS 16
 /* Largest hidden size: the kernel keeps a whole token row in registers. */
 #define TW_MAX_HIDDEN 32768
+/* Experts of one router, experts chosen per token (also the expert rows that
+ * one combine call sums per token), and groups of experts. */
+#define TW_MAX_EXPERTS 1024
+#define TW_MAX_TOPK 32
+#define TW_MAX_EXPERT_GROUPS 32
 
 typedef enum {
   TW_OK = 0,
   TW_ERR_INVALID_ARG = 1, /* null pointer, count or size out of range, overlap */
-  TW_ERR_ALIGN = 2,       /* H % 8 != 0 or a pointer not 16-byte aligned */
-  TW_ERR_UNSUPPORTED = 3, /* H > TW_MAX_HIDDEN */
+  TW_ERR_ALIGN = 2,       /* H % 8 != 0, H % group != 0, or a pointer not aligned */
+  TW_ERR_UNSUPPORTED = 3, /* H > TW_MAX_HIDDEN or E > TW_MAX_EXPERTS */
   TW_ERR_CUDA = 4,        /* a CUDA runtime call or launch failed */
   TW_ERR_DEVICE = 5       /* a kernel gave up on a bounded wait (see tw_device_status) */
 } tw_status;
@@ -122,6 +128,133 @@ typedef enum {
 TW_API int tw_fused_reduce_residual_rmsnorm(const void* const* partials, int N, void* residual,
                                      const void* gamma, float eps, int64_t T, int64_t H,
                                      void* out, tw_stream_t stream, int sm_budget);
+
+/* Scales of an e4m3 output: fp32, or a power of two as its biased exponent in
+ * one byte (E8M0, the scale type of the block-scaled 8-bit matrix products). */
+typedef enum { TW_SCALE_F32 = 0, TW_SCALE_E8M0 = 1 } tw_scale_type;
+
+/*
+ * tw_fused_reduce_residual_rmsnorm_q8 -- the fused step with its output in 8
+ * bits, for a projection that takes e4m3 operands with scales.
+ *
+ * As tw_fused_reduce_residual_rmsnorm up to the fp32 value
+ *     y = (z * r) * gamma,
+ * which is not rounded to bf16 but goes to e4m3 with one scale per group of
+ * `group` consecutive values of a row. With a = max |y| over the group:
+ *     s = max(a / 448, 2^-126)                              TW_SCALE_F32
+ *     s = the smallest power of two >= a / 448, >= 2^-126   TW_SCALE_E8M0
+ *     out = e4m3_rne(y / s)          y as the reader sees it: out * s
+ * The residual is bitwise that of the bf16 step. The bytes moved are
+ * (N+2)*T*H*2 + T*H plus the scales.
+ *
+ *   out        device e4m3 (one byte each) [T, H], 8-byte aligned; it may
+ *              overlap nothing else.
+ *   scales     device [T, H / group] (group 0: [T, 1]), row-major, float or
+ *              one byte; it may overlap nothing else.
+ *   group      32, 64 or 128, dividing H; 0: the whole row is one group.
+ *   scale_type a tw_scale_type.
+ *   Other arguments as for the bf16 step.
+ *
+ * A group of zeros has codes 0 and the smallest scale. NaN has e4m3's NaN
+ * code and takes no part in a; where a is infinite, s is infinite
+ * (E8M0: NaN), so that the group reads back as NaN.
+ *
+ * Errors: as the bf16 step, TW_ERR_INVALID_ARG for another group or scale
+ * type, TW_ERR_ALIGN for H % group != 0 or scales not aligned to their type.
+ */
+TW_API int tw_fused_reduce_residual_rmsnorm_q8(const void* const* partials, int N, void* residual,
+                                        const void* gamma, float eps, int64_t T, int64_t H,
+                                        void* out, void* scales, int group, int scale_type,
+                                        tw_stream_t stream, int sm_budget);
+
+/*
+ * tw_combine_residual_rmsnorm -- the step after the experts of a
+ * mixture-of-experts layer: the token's weighted expert rows are gathered and
+ * summed where the dense step sums its partials, in the same pass.
+ *
+ *     z       = sum_k weights[t,k] * X[rows[t,k]]   fp32 fma, k = 0 .. K-1
+ *               + P_0[t] + ... + P_{N-1}[t] + R[t]   fp32, in this order
+ *     R[t]    = bf16_rne(z)                           in place
+ *     out[t]  = bf16_rne( (z * r) * gamma ),  r = rsqrt(sum_j z_j^2 / H + eps)
+ *
+ *   experts    device bf16 [M, H]: the expert rows X, in any order; read only.
+ *              May be NULL when M == 0.
+ *   M          rows of X, 0 .. 2^31 - 1.
+ *   rows       device int32 [T, K]: the row of X of each slot. -1 (a dropped
+ *              slot) adds nothing and its weight is not used. Any other index
+ *              outside [0, M) is not read and adds nothing either, and sets
+ *              bit 3 of tw_device_status. A row may be named any number of
+ *              times.
+ *   weights    device float [T, K].
+ *   K          1 .. TW_MAX_TOPK.
+ *   partials   host array of N device pointers, bf16 [T, H], read only: dense
+ *              contributions such as a shared expert's output, one per rank.
+ *              May be NULL when N == 0.
+ *   N          0 .. TW_MAX_PARTIALS.
+ *   residual, gamma, eps, T, H, stream, sm_budget as for the fused step.
+ *   out        device bf16 [T, H]; it may be exactly one partial's buffer, no
+ *              other overlap. residual may overlap nothing else.
+ *
+ * Rows of the output are independent, as in the fused step. Errors as there,
+ * with TW_ERR_INVALID_ARG for M or K out of range and TW_ERR_ALIGN for rows
+ * or weights that are not 4-byte aligned.
+ */
+TW_API int tw_combine_residual_rmsnorm(const void* experts, int64_t M, const int32_t* rows,
+                                const float* weights, int K, const void* const* partials, int N,
+                                void* residual, const void* gamma, float eps, int64_t T, int64_t H,
+                                void* out, tw_stream_t stream, int sm_budget);
+
+/* The combine step with its output in e4m3 with scales: out, scales, group and
+ * scale_type as for tw_fused_reduce_residual_rmsnorm_q8. */
+TW_API int tw_combine_residual_rmsnorm_q8(const void* experts, int64_t M, const int32_t* rows,
+                                   const float* weights, int K, const void* const* partials, int N,
+                                   void* residual, const void* gamma, float eps, int64_t T,
+                                   int64_t H, void* out, void* scales, int group, int scale_type,
+                                   tw_stream_t stream, int sm_budget);
+
+/* Types of a router's logits, and its scores. */
+typedef enum { TW_LOGITS_F32 = 0, TW_LOGITS_BF16 = 1 } tw_logits_type;
+typedef enum { TW_SCORE_SOFTMAX = 0, TW_SCORE_SIGMOID = 1 } tw_score_type;
+
+/*
+ * tw_route_experts -- the experts of every token and their weights.
+ *
+ *     s_e  = softmax(logits[t])_e   or   1 / (1 + exp(-logits[t,e]))
+ *     c_e  = s_e + bias_e           (c_e = s_e without a bias)
+ *     groups of E / n_groups consecutive experts: a group's value is the sum
+ *            of its group_top largest c_e; the top_groups largest groups stay
+ *     ids[t]     = the K experts of those groups with the largest c_e, in
+ *                  descending order
+ *     weights[t] = s of those experts (without the bias), divided by their
+ *                  sum if renormalize, times scale
+ *
+ * The order is that of exact arithmetic: values that fp32 cannot tell apart
+ * are compared in fp64. Equal values go to the lowest index, and without a
+ * bias experts are ordered by their logits, which order the scores. A logit of
+ * -inf or NaN, or a bias of -inf or NaN, leaves an expert out; infinite
+ * positive values count as the largest finite one. A slot for which no expert
+ * is left has id -1 and weight 0, so a token with every logit at -inf has all
+ * its ids -1.
+ *
+ *   logits      device [T, E], fp32 or bf16 (logits_type), read only; aligned
+ *               to its type.
+ *   bias        device float [E] or NULL.
+ *   E           1 .. TW_MAX_EXPERTS.   K  1 .. min(TW_MAX_TOPK, experts of
+ *               top_groups groups).
+ *   n_groups    1 .. TW_MAX_EXPERT_GROUPS, dividing E; top_groups 1 ..
+ *               n_groups; group_top 1 or 2, at most E / n_groups.
+ *   scale       finite.
+ *   weights     device float [T, K], ids device int32 [T, K], written; they
+ *               overlap nothing.
+ *   T           >= 0; T == 0 is a no-op.
+ *
+ * Errors: TW_ERR_INVALID_ARG (a count, type or pointer as above, an overlap),
+ * TW_ERR_ALIGN, TW_ERR_UNSUPPORTED (E > TW_MAX_EXPERTS), TW_ERR_CUDA.
+ */
+TW_API int tw_route_experts(const void* logits, int logits_type, const float* bias, int64_t T, int E,
+                     int K, int scoring, int n_groups, int top_groups, int group_top,
+                     int renormalize, float scale, float* weights, int32_t* ids,
+                     tw_stream_t stream);
 
 /*
  * Offsets and threshold for tw_wave_split. Pass NULL for the pages' values:
@@ -299,7 +432,8 @@ TW_API int tw_launch_shape(int64_t T, int64_t H, int N, int sm_budget, int* grid
  * the outputs of some call since the last reset are not valid). Synchronises
  * the current device first. *code: 0 none; bit 0 a consumer gave up waiting
  * for staged data; bit 1 the producer gave up waiting for a free stage; bit 2
- * a final drain of in-flight copies gave up.
+ * a final drain of in-flight copies gave up; bit 3 a combine call met a row
+ * index outside its expert rows (nothing was read there).
  */
 TW_API int tw_device_status(int reset, int* code);
 

@@ -23,11 +23,23 @@ The functions carry the C names:
     tw_add_rmsnorm(sum_in, residual, gamma, eps, out, stream=None)     # unfused baseline
     tw_shard_rows(num_tokens, world, rank)                              # token-boundary shard
 
+Around the experts of a mixture-of-experts layer, and before 8-bit products:
+
+    tw_fused_reduce_residual_rmsnorm_q8(partials, residual, gamma, eps, out, scales, group=0,
+                                        stream=None, sm_budget=0)       # e4m3 output with scales
+    tw_route_experts(logits, weights, ids, bias=None, scoring="softmax", n_groups=1, top_groups=1,
+                     group_top=1, renormalize=True, scale=1.0, stream=None)
+    tw_combine_residual_rmsnorm(experts, rows, weights, residual, gamma, eps, out, partials=(),
+                                stream=None, sm_budget=0)
+    tw_combine_residual_rmsnorm_q8(experts, rows, weights, residual, gamma, eps, out, scales,
+                                   group=0, partials=(), stream=None, sm_budget=0)
+
 The token-shard form of the step across tensor-parallel ranks (all-to-all,
 fused step on the rank's shard, all-gather) is ``shard.TokenShardStep``.
 
-For launch-bound loops, ``FusedCall``, ``SplitCall``, ``WaveSplitCall`` and
-``PlannedSplitCall`` marshal the arguments once and then make a single ctypes
+For launch-bound loops, ``FusedCall``, ``SplitCall``, ``WaveSplitCall``,
+``PlannedSplitCall``, ``FusedQ8Call``, ``RouteCall``, ``CombineCall`` and
+``CombineQ8Call`` marshal the arguments once and then make a single ctypes
 call each time they are called.
 """
 
@@ -45,6 +57,14 @@ TW_ERR_CUDA = 4
 TW_ERR_DEVICE = 5
 TW_MAX_PARTIALS = 16
 TW_MAX_HIDDEN = 32768
+TW_MAX_EXPERTS = 1024
+TW_MAX_TOPK = 32
+TW_MAX_EXPERT_GROUPS = 32
+TW_SCALE_F32 = 0
+TW_SCALE_E8M0 = 1
+TW_LOGITS_F32 = 0
+TW_LOGITS_BF16 = 1
+TW_SCORES = {"softmax": 0, "sigmoid": 1}
 
 DEFAULT_OFFSETS = (0, 64, 128, 192, 256, 512)
 DEFAULT_MIN_SPLIT_TOKENS = 1024
@@ -52,7 +72,8 @@ DEFAULT_MIN_SPLIT_TOKENS = 1024
 EXPORTED = ("tw_fused_reduce_residual_rmsnorm", "tw_wave_split", "tw_run_split", "tw_strerror",
             "tw_launch_shape", "tw_device_status", "tw_fused_debug_smid", "tw_reduce_partials",
             "tw_add_rmsnorm", "tw_run_split_after", "tw_split_lookup", "tw_debug_wait_timeout",
-            "tw_run_wave_split", "tw_shard_rows")
+            "tw_run_wave_split", "tw_shard_rows", "tw_fused_reduce_residual_rmsnorm_q8",
+            "tw_combine_residual_rmsnorm", "tw_combine_residual_rmsnorm_q8", "tw_route_experts")
 
 
 class TwError(RuntimeError):
@@ -120,6 +141,17 @@ def lib():
     L.tw_add_rmsnorm.restype = _int
     L.tw_shard_rows.argtypes = [_i64, _int, _int, ctypes.POINTER(_i64), ctypes.POINTER(_i64)]
     L.tw_shard_rows.restype = _int
+    f32 = ctypes.c_float
+    q8 = [_vp, _vp, _int, _int, _vp, _int]  # out, scales, group, scale type, stream, SM budget
+    L.tw_fused_reduce_residual_rmsnorm_q8.argtypes = [ctypes.POINTER(_vp), _int, _vp, _vp, f32,
+                                                      _i64, _i64] + q8
+    combine = [_vp, _i64, _vp, _vp, _int, ctypes.POINTER(_vp), _int, _vp, _vp, f32, _i64, _i64]
+    L.tw_combine_residual_rmsnorm.argtypes = combine + [_vp, _vp, _int]
+    L.tw_combine_residual_rmsnorm_q8.argtypes = combine + q8
+    L.tw_route_experts.argtypes = [_vp, _int, _vp, _i64] + [_int] * 7 + [f32, _vp, _vp, _vp]
+    for name in ("tw_fused_reduce_residual_rmsnorm_q8", "tw_combine_residual_rmsnorm",
+                 "tw_combine_residual_rmsnorm_q8", "tw_route_experts"):
+        getattr(L, name).restype = _int
     _lib = L
     return L
 
@@ -218,17 +250,20 @@ def _check_devices(where, tensors=(), streams=()):
                              "and streams must be on the current device" % (where, name, d, dev))
 
 
-def _step_args(partials, residual, gamma, out, where="fused step", streams=()):
+def _step_args(partials, residual, gamma, out, where="fused step", streams=(), more=(),
+               bf16_out=True):
     """Validated (pointer array, N, T, H) for a fused step's tensors. An
     [N, T, H] stack is checked once and its N pointers are computed from its
     base address and stride. Every tensor and stream must be on the current
-    device (_check_devices)."""
+    device (_check_devices), as must ``more``, (name, tensor) pairs whose
+    layout the caller has checked; bf16_out False: so has out's been."""
     import torch
     T, H = _shape(residual)
     _check_tensor(residual, "residual", (T, H))
     _check_tensor(gamma, "gamma", (H,))
-    _check_tensor(out, "out", (T, H))
-    named = [("residual", residual), ("gamma", gamma), ("out", out)]
+    if bf16_out:
+        _check_tensor(out, "out", (T, H))
+    named = [("residual", residual), ("gamma", gamma), ("out", out)] + list(more)
     if isinstance(partials, torch.Tensor) and partials.dim() == 3:
         n = int(partials.shape[0])
         if not (partials.dtype is torch.bfloat16 and partials.is_cuda and
@@ -283,6 +318,75 @@ def tw_fused_debug_smid(partials, residual, gamma, eps, out, smid_out, stream=No
     st = lib().tw_fused_debug_smid(arr, n, _ptr(residual), _ptr(gamma), float(eps), T, H, _ptr(out),
                                    _stream(stream), int(sm_budget), _ptr(smid_out))
     _check(st, "tw_fused_debug_smid")
+
+
+def _check_typed(t, name, shape, dtypes):
+    """A contiguous CUDA tensor of the given shape and one of the dtypes."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype not in dtypes or not t.is_cuda or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous CUDA tensor of %s (got %s, %s, contiguous=%s)"
+                         % (name, " or ".join(str(d) for d in dtypes), t.dtype, t.device,
+                            t.is_contiguous()))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+
+
+def _q8_args(residual, out, scales, group):
+    """Validated (group, scale type) of an e4m3 output: out float8_e4m3fn
+    [T, H], scales float32 or float8_e8m0fnu [T, H / group] ([T, 1] for
+    group 0). Groups that the C call refuses are left to it."""
+    import torch
+    T, H = _shape(residual)
+    group = int(group)
+    _check_typed(out, "out", (T, H), (torch.float8_e4m3fn,))
+    per_row = H // group if group > 0 and H % group == 0 else 1
+    _check_typed(scales, "scales", (T, per_row), (torch.float32, torch.float8_e8m0fnu))
+    return group, TW_SCALE_F32 if scales.dtype is torch.float32 else TW_SCALE_E8M0
+
+
+def tw_fused_reduce_residual_rmsnorm_q8(partials, residual, gamma, eps, out, scales, group=0,
+                                        stream=None, sm_budget=0):
+    """The fused step with an e4m3 output: out float8_e4m3fn [T, H] and one
+    scale per ``group`` (32, 64, 128; 0: the row) values in ``scales``,
+    [T, H / group], float32 or float8_e8m0fnu (power-of-two scales). The value
+    of a code is code * scale. ``residual`` is updated as by the bf16 step."""
+    FusedQ8Call(partials, residual, gamma, eps, out, scales, group, stream, sm_budget)()
+
+
+def tw_combine_residual_rmsnorm(experts, rows, weights, residual, gamma, eps, out, partials=(),
+                                stream=None, sm_budget=0):
+    """residual <- bf16(z), out <- RMSNorm(z) with z = sum_k weights[t, k] *
+    experts[rows[t, k]] + sum of the partials + residual.
+
+    experts: bf16 [M, H]; rows: int32 [T, K], -1 for a dropped slot; weights:
+    float32 [T, K]; partials: none, a list of bf16 [T, H] or one [N, T, H]
+    tensor; the rest as for the fused step. A row index outside [0, M) other
+    than -1 adds nothing and sets bit 3 of ``tw_device_status``."""
+    CombineCall(experts, rows, weights, residual, gamma, eps, out, partials, stream, sm_budget)()
+
+
+def tw_combine_residual_rmsnorm_q8(experts, rows, weights, residual, gamma, eps, out, scales,
+                                   group=0, partials=(), stream=None, sm_budget=0):
+    """The combine step with an e4m3 output; out, scales and group as for
+    tw_fused_reduce_residual_rmsnorm_q8."""
+    CombineQ8Call(experts, rows, weights, residual, gamma, eps, out, scales, group, partials,
+                  stream, sm_budget)()
+
+
+def tw_route_experts(logits, weights, ids, bias=None, scoring="softmax", n_groups=1, top_groups=1,
+                     group_top=1, renormalize=True, scale=1.0, stream=None):
+    """The K experts of every token and their weights.
+
+    logits: float32 or bf16 [T, E]; weights: float32 [T, K] and ids: int32
+    [T, K], written; bias: float32 [E], added to the scores for the choice
+    only; scoring "softmax" or "sigmoid"; n_groups > 1: only the top_groups
+    groups of experts with the largest sum of their group_top best values are
+    chosen from. Ties go to the lowest index; a slot with no expert left has
+    id -1 and weight 0."""
+    RouteCall(logits, weights, ids, bias, scoring, n_groups, top_groups, group_top, renormalize,
+              scale, stream)()
 
 
 def _opts_arg(offsets, min_split_tokens):
@@ -434,6 +538,113 @@ class FusedCall:
         st = self._fn(*self._args)
         if st != TW_OK:
             raise TwError(st, "tw_fused_reduce_residual_rmsnorm")
+
+
+class _PreparedCall:
+    """A C call with its arguments marshalled once; holds the tensors."""
+
+    def _prepare(self, name, args, tensors):
+        self.tensors = tensors
+        self._name = name
+        self._fn = getattr(lib(), name)
+        self._args = args
+
+    def __call__(self):
+        st = self._fn(*self._args)
+        if st != TW_OK:
+            raise TwError(st, self._name)
+
+
+class FusedQ8Call(_PreparedCall):
+    """tw_fused_reduce_residual_rmsnorm_q8 with its arguments marshalled once."""
+
+    def __init__(self, partials, residual, gamma, eps, out, scales, group=0, stream=None,
+                 sm_budget=0):
+        group, scale_type = _q8_args(residual, out, scales, group)
+        where = "tw_fused_reduce_residual_rmsnorm_q8"
+        arr, n, T, H = _step_args(partials, residual, gamma, out, where, [("stream", stream)],
+                                  [("scales", scales)], bf16_out=False)
+        self._prepare(where, (arr, _int(n), _ptr(residual), _ptr(gamma), ctypes.c_float(eps),
+                              _i64(T), _i64(H), _ptr(out), _ptr(scales), _int(group),
+                              _int(scale_type), _stream(stream), _int(int(sm_budget))),
+                      (partials, residual, gamma, out, scales))
+
+
+def _combine_args(where, experts, rows, weights, residual, gamma, eps, out, partials, stream,
+                  more=(), bf16_out=True):
+    """The C call's arguments up to out, from validated tensors."""
+    import torch
+    T, H = _shape(residual)
+    if not isinstance(rows, torch.Tensor) or rows.dim() != 2:
+        raise ValueError("rows must be an int32 [T, K] tensor")
+    if not isinstance(experts, torch.Tensor) or experts.dim() != 2:
+        raise ValueError("experts must be a bf16 [M, H] tensor")
+    K, M = int(rows.shape[1]), int(experts.shape[0])
+    _check_typed(rows, "rows", (T, K), (torch.int32,))
+    _check_typed(weights, "weights", (T, K), (torch.float32,))
+    _check_tensor(experts, "experts", (M, H))
+    arr, n, T, H = _step_args(partials, residual, gamma, out, where, [("stream", stream)],
+                              [("experts", experts), ("rows", rows), ("weights", weights)] +
+                              list(more), bf16_out)
+    return (_ptr(experts), _i64(M), _ptr(rows), _ptr(weights), _int(K), arr, _int(n),
+            _ptr(residual), _ptr(gamma), ctypes.c_float(eps), _i64(T), _i64(H))
+
+
+class CombineCall(_PreparedCall):
+    """tw_combine_residual_rmsnorm with its arguments marshalled once."""
+
+    def __init__(self, experts, rows, weights, residual, gamma, eps, out, partials=(), stream=None,
+                 sm_budget=0):
+        where = "tw_combine_residual_rmsnorm"
+        args = _combine_args(where, experts, rows, weights, residual, gamma, eps, out, partials,
+                             stream)
+        self._prepare(where, args + (_ptr(out), _stream(stream), _int(int(sm_budget))),
+                      (experts, rows, weights, residual, gamma, out, partials))
+
+
+class CombineQ8Call(_PreparedCall):
+    """tw_combine_residual_rmsnorm_q8 with its arguments marshalled once."""
+
+    def __init__(self, experts, rows, weights, residual, gamma, eps, out, scales, group=0,
+                 partials=(), stream=None, sm_budget=0):
+        where = "tw_combine_residual_rmsnorm_q8"
+        group, scale_type = _q8_args(residual, out, scales, group)
+        args = _combine_args(where, experts, rows, weights, residual, gamma, eps, out, partials,
+                             stream, [("scales", scales)], bf16_out=False)
+        self._prepare(where, args + (_ptr(out), _ptr(scales), _int(group), _int(scale_type),
+                                     _stream(stream), _int(int(sm_budget))),
+                      (experts, rows, weights, residual, gamma, out, scales, partials))
+
+
+class RouteCall(_PreparedCall):
+    """tw_route_experts with its arguments marshalled once."""
+
+    def __init__(self, logits, weights, ids, bias=None, scoring="softmax", n_groups=1,
+                 top_groups=1, group_top=1, renormalize=True, scale=1.0, stream=None):
+        import torch
+        where = "tw_route_experts"
+        if scoring not in TW_SCORES:
+            raise ValueError("scoring must be one of %s" % sorted(TW_SCORES))
+        for name, t in (("logits", logits), ("weights", weights)):
+            if not isinstance(t, torch.Tensor) or t.dim() != 2:
+                raise ValueError("%s must be a two-dimensional tensor" % name)
+        T, E = (int(n) for n in logits.shape)
+        K = int(weights.shape[1])
+        _check_typed(logits, "logits", (T, E), (torch.float32, torch.bfloat16))
+        _check_typed(weights, "weights", (T, K), (torch.float32,))
+        _check_typed(ids, "ids", (T, K), (torch.int32,))
+        named = [("logits", logits), ("weights", weights), ("ids", ids)]
+        if bias is not None:
+            _check_typed(bias, "bias", (E,), (torch.float32,))
+            named.append(("bias", bias))
+        _check_devices(where, named, [("stream", stream)])
+        self._prepare(where, (_ptr(logits), _int(TW_LOGITS_F32 if logits.dtype is torch.float32
+                                                 else TW_LOGITS_BF16), _ptr(bias), _i64(T),
+                              _int(E), _int(K), _int(TW_SCORES[scoring]), _int(int(n_groups)),
+                              _int(int(top_groups)), _int(int(group_top)),
+                              _int(1 if renormalize else 0), ctypes.c_float(scale), _ptr(weights),
+                              _ptr(ids), _stream(stream)),
+                      (logits, weights, ids, bias))
 
 
 class WaveSplitCall:

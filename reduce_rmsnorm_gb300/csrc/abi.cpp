@@ -305,6 +305,195 @@ extern "C" int tw_add_rmsnorm(const void* sum, void* residual, const void* gamma
   }
 }
 
+namespace {
+
+template <typename P>
+bool aligned_to(const void* p) { return (reinterpret_cast<uintptr_t>(p) & (sizeof(P) - 1)) == 0; }
+
+// Scale group and type of an e4m3 output; group 0 is the whole row.
+int validate_q8(int64_t H, int group, int scale_type) {
+  if (scale_type != TW_SCALE_F32 && scale_type != TW_SCALE_E8M0) return TW_ERR_INVALID_ARG;
+  if (group != 0 && group != 32 && group != 64 && group != 128) return TW_ERR_INVALID_ARG;
+  if (group != 0 && H % group != 0) return TW_ERR_ALIGN;
+  return TW_OK;
+}
+
+// Validation of one combine call over rows [0, T); fills the kernel args
+// (T > 0). scale_type < 0: bf16 output.
+int validate_combine(const void* experts, int64_t M, const int32_t* rows, const float* weights,
+                     int K, const void* const* partials, int N, void* residual, const void* gamma,
+                     float eps, int64_t T, int64_t H, void* out, void* scales, int group,
+                     int scale_type, int sm_budget, tw::CombineArgs* a) {
+  if (N < 0 || N > TW_MAX_PARTIALS || K < 1 || K > TW_MAX_TOPK) return TW_ERR_INVALID_ARG;
+  if (M < 0 || M > INT32_MAX) return TW_ERR_INVALID_ARG;
+  const bool q8 = scale_type >= 0;
+  int st = validate_shape(1, eps, T, H, sm_budget);
+  if (st != TW_OK) return st;
+  if (q8 && (st = validate_q8(H, group, scale_type)) != TW_OK) return st;
+  if (T > INT64_MAX / 8 / K) return TW_ERR_INVALID_ARG;
+  if (T == 0) return TW_OK;
+  if (!rows || !weights || !residual || !gamma || !out || (M > 0 && !experts) ||
+      (N > 0 && !partials) || (q8 && !scales))
+    return TW_ERR_INVALID_ARG;
+  for (int r = 0; r < N; ++r)
+    if (!partials[r]) return TW_ERR_INVALID_ARG;
+  for (int r = 0; r < N; ++r)
+    if (!aligned16(partials[r])) return TW_ERR_ALIGN;
+  if (!aligned16(experts) || !aligned16(residual) || !aligned16(gamma)) return TW_ERR_ALIGN;
+  if (!aligned_to<float>(rows) || !aligned_to<float>(weights)) return TW_ERR_ALIGN;
+  if (q8 ? !aligned_to<int64_t>(out) : !aligned16(out)) return TW_ERR_ALIGN;
+  if (q8 && scale_type == TW_SCALE_F32 && !aligned_to<float>(scales)) return TW_ERR_ALIGN;
+  // The written tensors overlap nothing else, except that a bf16 out may be
+  // exactly one partial: a row's partials are all read before its output is
+  // written, by the CTA that owns the row.
+  const int64_t bytes = T * H * 2;
+  struct Span { const void* p; int64_t n; };
+  const Span written[3] = {{residual, bytes}, {out, q8 ? T * H : bytes},
+                           {scales, q8 ? T * (group ? H / group : 1) *
+                                             (scale_type == TW_SCALE_F32 ? 4 : 1) : 0}};
+  const Span read[4] = {{gamma, H * 2}, {rows, T * K * 4}, {weights, T * K * 4},
+                        {experts, M * H * 2}};
+  const int n_written = q8 ? 3 : 2;
+  for (int i = 0; i < n_written; ++i) {
+    const Span& w = written[i];
+    for (int j = 0; j < i; ++j)
+      if (overlap(w.p, w.n, written[j].p, written[j].n)) return TW_ERR_INVALID_ARG;
+    for (const Span& r : read)
+      if (r.n > 0 && overlap(w.p, w.n, r.p, r.n)) return TW_ERR_INVALID_ARG;
+    for (int r = 0; r < N; ++r)
+      if (overlap(w.p, w.n, partials[r], bytes) && !(!q8 && w.p == out && out == partials[r]))
+        return TW_ERR_INVALID_ARG;
+  }
+  a->experts = experts;
+  a->m = M;
+  a->rows = rows;
+  a->weights = weights;
+  a->k = K;
+  for (int r = 0; r < N; ++r) a->partials[r] = partials[r];
+  a->n = N;
+  a->residual = residual;
+  a->gamma = gamma;
+  a->out = out;
+  a->scales = scales;
+  a->group = static_cast<int>(group ? group : H);
+  a->scale_type = scale_type;
+  a->eps = eps;
+  a->tokens = T;
+  a->hidden = H;
+  return TW_OK;
+}
+
+}  // namespace
+
+extern "C" int tw_combine_residual_rmsnorm(const void* experts, int64_t M, const int32_t* rows,
+                                           const float* weights, int K,
+                                           const void* const* partials, int N, void* residual,
+                                           const void* gamma, float eps, int64_t T, int64_t H,
+                                           void* out, tw_stream_t stream, int sm_budget) {
+  try {
+    tw::CombineArgs a;
+    const int st = validate_combine(experts, M, rows, weights, K, partials, N, residual, gamma, eps,
+                                    T, H, out, nullptr, 0, -1, sm_budget, &a);
+    if (st != TW_OK || T == 0) return st;
+    return tw::launch_combine(a, reinterpret_cast<cudaStream_t>(stream), sm_budget);
+  } catch (...) {
+    return TW_ERR_CUDA;
+  }
+}
+
+extern "C" int tw_combine_residual_rmsnorm_q8(const void* experts, int64_t M, const int32_t* rows,
+                                              const float* weights, int K,
+                                              const void* const* partials, int N, void* residual,
+                                              const void* gamma, float eps, int64_t T, int64_t H,
+                                              void* out, void* scales, int group, int scale_type,
+                                              tw_stream_t stream, int sm_budget) {
+  try {
+    if (scale_type < 0) return TW_ERR_INVALID_ARG;
+    tw::CombineArgs a;
+    const int st = validate_combine(experts, M, rows, weights, K, partials, N, residual, gamma, eps,
+                                    T, H, out, scales, group, scale_type, sm_budget, &a);
+    if (st != TW_OK || T == 0) return st;
+    return tw::launch_combine(a, reinterpret_cast<cudaStream_t>(stream), sm_budget);
+  } catch (...) {
+    return TW_ERR_CUDA;
+  }
+}
+
+extern "C" int tw_fused_reduce_residual_rmsnorm_q8(const void* const* partials, int N,
+                                                   void* residual, const void* gamma, float eps,
+                                                   int64_t T, int64_t H, void* out, void* scales,
+                                                   int group, int scale_type, tw_stream_t stream,
+                                                   int sm_budget) {
+  try {
+    if (N < 1 || scale_type < 0) return TW_ERR_INVALID_ARG;
+    // no slot: the dense sum alone; one row index and weight stand in for the
+    // checks of the (unused) slot arrays
+    static const int32_t no_row = -1;
+    static const float no_weight = 0.0f;
+    tw::CombineArgs a;
+    const int st = validate_combine(nullptr, 0, &no_row, &no_weight, 1, partials, N, residual,
+                                    gamma, eps, T, H, out, scales, group, scale_type, sm_budget,
+                                    &a);
+    if (st != TW_OK || T == 0) return st;
+    a.k = 0;
+    a.rows = nullptr;
+    a.weights = nullptr;
+    return tw::launch_combine(a, reinterpret_cast<cudaStream_t>(stream), sm_budget);
+  } catch (...) {
+    return TW_ERR_CUDA;
+  }
+}
+
+extern "C" int tw_route_experts(const void* logits, int logits_type, const float* bias, int64_t T,
+                                int E, int K, int scoring, int n_groups, int top_groups,
+                                int group_top, int renormalize, float scale, float* weights,
+                                int32_t* ids, tw_stream_t stream) {
+  try {
+    if (logits_type != TW_LOGITS_F32 && logits_type != TW_LOGITS_BF16) return TW_ERR_INVALID_ARG;
+    if (scoring != TW_SCORE_SOFTMAX && scoring != TW_SCORE_SIGMOID) return TW_ERR_INVALID_ARG;
+    if (T < 0 || E < 1 || K < 1 || K > TW_MAX_TOPK) return TW_ERR_INVALID_ARG;
+    if (n_groups < 1 || n_groups > TW_MAX_EXPERT_GROUPS || E % n_groups != 0 || top_groups < 1 ||
+        top_groups > n_groups)
+      return TW_ERR_INVALID_ARG;
+    const int group_size = E / n_groups;
+    if (group_top < 1 || group_top > 2 || group_top > group_size) return TW_ERR_INVALID_ARG;
+    if (K > static_cast<int64_t>(top_groups) * group_size) return TW_ERR_INVALID_ARG;
+    if (!std::isfinite(scale)) return TW_ERR_INVALID_ARG;
+    if (E > TW_MAX_EXPERTS) return TW_ERR_UNSUPPORTED;
+    if (T > INT64_MAX / 8 / TW_MAX_EXPERTS) return TW_ERR_INVALID_ARG;
+    if (T == 0) return TW_OK;
+    if (!logits || !weights || !ids) return TW_ERR_INVALID_ARG;
+    if (logits_type == TW_LOGITS_F32 ? !aligned_to<float>(logits) : !aligned_to<int16_t>(logits))
+      return TW_ERR_ALIGN;
+    if (!aligned_to<float>(weights) || !aligned_to<float>(ids) || (bias && !aligned_to<float>(bias)))
+      return TW_ERR_ALIGN;
+    const int64_t in = T * E * (logits_type == TW_LOGITS_F32 ? 4 : 2), out = T * K * 4;
+    if (overlap(weights, out, ids, out)) return TW_ERR_INVALID_ARG;
+    for (const void* w : {static_cast<const void*>(weights), static_cast<const void*>(ids)}) {
+      if (overlap(w, out, logits, in)) return TW_ERR_INVALID_ARG;
+      if (bias && overlap(w, out, bias, static_cast<int64_t>(E) * 4)) return TW_ERR_INVALID_ARG;
+    }
+    tw::RouteArgs a;
+    a.logits = logits;
+    a.logits_type = logits_type;
+    a.bias = bias;
+    a.tokens = T;
+    a.experts = E;
+    a.k = K;
+    a.scoring = scoring;
+    a.n_groups = n_groups;
+    a.top_groups = top_groups;
+    a.group_top = group_top;
+    a.renormalize = renormalize != 0;
+    a.scale = scale;
+    a.weights = weights;
+    a.ids = ids;
+    return tw::launch_route(a, reinterpret_cast<cudaStream_t>(stream));
+  } catch (...) {
+    return TW_ERR_CUDA;
+  }
+}
+
 extern "C" int tw_launch_shape(int64_t T, int64_t H, int N, int sm_budget, int* grid, int* threads,
                                int* smem_bytes, int* stages) {
   try {
@@ -345,8 +534,8 @@ extern "C" const char* tw_strerror(int status) {
   switch (status) {
     case TW_OK: return "TW_OK: success";
     case TW_ERR_INVALID_ARG: return "TW_ERR_INVALID_ARG: invalid argument";
-    case TW_ERR_ALIGN: return "TW_ERR_ALIGN: H must be a multiple of 8 and pointers 16-byte aligned";
-    case TW_ERR_UNSUPPORTED: return "TW_ERR_UNSUPPORTED: hidden size above TW_MAX_HIDDEN";
+    case TW_ERR_ALIGN: return "TW_ERR_ALIGN: H must be a multiple of 8 (and of the scale group) and pointers aligned";
+    case TW_ERR_UNSUPPORTED: return "TW_ERR_UNSUPPORTED: hidden size above TW_MAX_HIDDEN or experts above TW_MAX_EXPERTS";
     case TW_ERR_CUDA: return "TW_ERR_CUDA: a CUDA runtime call or kernel launch failed";
     case TW_ERR_DEVICE: return "TW_ERR_DEVICE: a kernel gave up on a bounded wait";
     default: return "unknown tw_status";

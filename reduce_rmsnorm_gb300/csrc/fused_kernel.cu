@@ -57,6 +57,7 @@
 #include <cstdint>
 #include <mutex>
 
+#include "row_ops.cuh"
 #include "tw_internal.h"
 
 namespace tw {
@@ -179,20 +180,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   return v;
 }
 
-// Asks L2 to fetch [src, src + bytes) (16-byte aligned, bytes a multiple of
-// 16). A hint only: nothing is returned to the thread and no memory is written.
-__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
-}
-
-__device__ __forceinline__ void grid_dependency_wait() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
-__device__ __forceinline__ void grid_launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 __device__ __forceinline__ uint32_t sm_id() {
   uint32_t id;
   asm volatile("mov.u32 %0, %%smid;" : "=r"(id));
@@ -244,70 +231,6 @@ __device__ void drain_ring(uint64_t* full, int stages, long long issued) {
     const long long it_last = last - ((last - st) % stages);
     drain_phase(&full[st], static_cast<uint32_t>((it_last / stages) & 1));
   }
-}
-
-// ------------------------------------------------------------------ bf16 x 8
-
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-
-__device__ __forceinline__ void load8(const uint4 q, float a[8]) {
-  a[0] = bf16_lo(q.x); a[1] = bf16_hi(q.x);
-  a[2] = bf16_lo(q.y); a[3] = bf16_hi(q.y);
-  a[4] = bf16_lo(q.z); a[5] = bf16_hi(q.z);
-  a[6] = bf16_lo(q.w); a[7] = bf16_hi(q.w);
-}
-
-// a[2i], a[2i+1] += the two bf16 values of word w, as one packed fp32x2 add
-// (add.rn.f32x2: two independent IEEE round-to-nearest fp32 additions, the
-// same results as two scalar adds, in one instruction).
-__device__ __forceinline__ void add2(float& lo, float& hi, uint32_t w) {
-  uint64_t acc, v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(acc) : "f"(lo), "f"(hi));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(w << 16), "r"(w & 0xffff0000u));
-  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(acc) : "l"(v));
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(acc));
-}
-
-__device__ __forceinline__ void add8(const uint4 q, float a[8]) {
-  add2(a[0], a[1], q.x);
-  add2(a[2], a[3], q.y);
-  add2(a[4], a[5], q.z);
-  add2(a[6], a[7], q.w);
-}
-
-// y[i] = (z[i] * rs) * gamma[i] for the 8 bf16 gamma values of q, as packed
-// fp32x2 multiplies (mul.rn.f32x2: two IEEE round-to-nearest products per
-// instruction, the same results as scalar multiplies in the same order).
-__device__ __forceinline__ void scale8(const float z[8], float rs, const uint4 q, float y[8]) {
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-  uint64_t r2;
-  asm("mov.b64 %0, {%1, %1};" : "=l"(r2) : "f"(rs));
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    uint64_t a, g;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(z[2 * k]), "f"(z[2 * k + 1]));
-    asm("mov.b64 %0, {%1, %2};" : "=l"(g) : "r"(w[k] << 16), "r"(w[k] & 0xffff0000u));
-    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(r2));
-    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(g));
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(y[2 * k]), "=f"(y[2 * k + 1]) : "l"(a));
-  }
-}
-
-// Sum of the 8 warp partials in warp order, read as two 16-byte loads.
-__device__ __forceinline__ float warp_total(const float* w8) {
-  const float4 a = *reinterpret_cast<const float4*>(w8);
-  const float4 b = *reinterpret_cast<const float4*>(w8 + 4);
-  return ((((((a.x + a.y) + a.z) + a.w) + b.x) + b.y) + b.z) + b.w;
-}
-
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-__device__ __forceinline__ uint4 pack8(const float a[8]) {
-  return make_uint4(pack2(a[0], a[1]), pack2(a[2], a[3]), pack2(a[4], a[5]), pack2(a[6], a[7]));
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -1275,7 +1198,10 @@ int read_device_error(int reset, int* code) {
     const unsigned int zero = 0;
     if (cudaMemcpyToSymbol(g_device_error, &zero, sizeof(zero)) != cudaSuccess) return TW_ERR_CUDA;
   }
-  if (code) *code = static_cast<int>(v);
+  unsigned combine = 0;
+  const int st = read_combine_error(reset, &combine);
+  if (st != TW_OK) return st;
+  if (code) *code = static_cast<int>(v | combine);
   return TW_OK;
 }
 

@@ -43,6 +43,48 @@ int launch_reduce(const void* const* partials, int n, int64_t rows, int64_t hidd
 int launch_add_rmsnorm(const void* sum, void* residual, const void* gamma, float eps, int64_t rows,
                        int64_t hidden, void* out, cudaStream_t stream);
 
+// Arguments of one combine launch, already validated. scale_type < 0: bf16
+// output; otherwise e4m3 with scales.
+struct CombineArgs {
+  const void* experts;
+  int64_t m;
+  const int32_t* rows;
+  const float* weights;
+  int k;
+  const void* partials[TW_MAX_PARTIALS];
+  int n;
+  void* residual;
+  const void* gamma;
+  void* out;
+  void* scales;
+  int group;  // values per scale (H for a whole row)
+  int scale_type;
+  float eps;
+  int64_t tokens;
+  int64_t hidden;
+};
+int launch_combine(const CombineArgs& a, cudaStream_t stream, int sm_budget);
+// Read (and optionally clear) the combine kernels' device-side error word,
+// after the device was synchronised.
+int read_combine_error(int reset, unsigned* code);
+
+// Arguments of one routing launch, already validated.
+struct RouteArgs {
+  const void* logits;
+  int logits_type;
+  const float* bias;
+  int64_t tokens;
+  int experts;
+  int k;
+  int scoring;
+  int n_groups, top_groups, group_top;
+  int renormalize;
+  float scale;
+  float* weights;
+  int32_t* ids;
+};
+int launch_route(const RouteArgs& a, cudaStream_t stream);
+
 // Diagnostic kernel: a bounded wait on an mbarrier nothing completes.
 int launch_wait_probe(long long limit_ns, cudaStream_t stream);
 
