@@ -122,6 +122,39 @@ def test_route_values_that_fp32_cannot_tell_apart(scoring):
 
 
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_route_near_values_with_fewer_experts_than_slots(scoring):
+    """Candidates that only fp64 can order, some rows with fewer than K of them."""
+    g = torch.Generator().manual_seed(12)
+    for E, K in ((64, 8), (64, 20), (256, 8), (300, 8), (6, 6)):
+        x = torch.randn(12, E, generator=g)
+        x[:] = x[0]
+        s = torch.softmax(x[0].double(), 0) if scoring == "softmax" else torch.sigmoid(x[0].double())
+        bias = (0.5 - s).float()
+        for t in range(8):
+            x[t, t + 1:] = -math.inf
+        if scoring == "softmax":  # the scores of the masked rows differ: no near values there
+            check(x[8:], K, bias, scoring=scoring)
+        check(x, K, bias, scoring=scoring)
+        check(x, K, bias, scoring=scoring, renormalize=False)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G,top", [(64, 8, 3), (128, 8, 4), (256, 8, 4), (256, 4, 2), (96, 12, 5)])
+def test_route_near_group_values(scoring, E, G, top):
+    """Group values that differ by less than fp32 holds, and groups that tie."""
+    g = torch.Generator().manual_seed(13)
+    size = E // G
+    x = torch.randn(4000, size, generator=g).repeat(1, G)
+    # one expert of each group moves by a few fp32 steps, in some rows not at all
+    x[::2, ::size] += 3e-7 * torch.randint(-2, 3, (2000, G), generator=g)
+    for bias in (None, torch.zeros(E), 0.01 * torch.randn(size, generator=g).repeat(G)):
+        for group_top in (1, 2):
+            check(x[:60], 4, bias, scoring=scoring, n_groups=G, top_groups=top, group_top=group_top)
+    ids, _ = route(x, 4, torch.zeros(E), scoring=scoring, n_groups=G, top_groups=top, group_top=2)
+    assert ids.min() >= 0
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 def test_route_masked_experts_and_rows(scoring):
     inf = math.inf
     x = logits(8, 40, seed=5)
@@ -179,6 +212,30 @@ def test_route_unaligned_rows_streams_and_neighbours():
         want, _ = experts.route(x.double().numpy(), K)
         assert np.array_equal(ids[1:-1].view(T, K).cpu().numpy(), want)
         assert w[0] == -3 and w[-1] == -3 and ids[0] == -9 and ids[-1] == -9
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E,K,G,top", [(256, 8, 1, 1), (256, 8, 8, 4), (96, 3, 1, 1), (128, 8, 4, 2),
+                                       (224, 7, 1, 1), (192, 8, 6, 3)])
+def test_route_long_batches(E, K, G, top, dtype, scoring):
+    """Enough tokens that rows of more than 64 experts share a warp. The batch
+    repeats 150 tokens, so that every place in a warp meets every one of them;
+    some are masked, some equal everywhere."""
+    x = logits(150, E, seed=E, dtype=dtype)
+    x[3], x[4, : E - 2], x[5], x[6, ::2] = -math.inf, -math.inf, 0.5, x[6, 1::2]
+    x[7] = math.nan
+    bias = logits(1, E, seed=2, sigma=0.05)[0]
+    many = x.repeat(220, 1)[:32797]
+    for b in (None, bias):
+        for renormalize in (True, False):
+            kw = dict(scoring=scoring, renormalize=renormalize, n_groups=G, top_groups=top,
+                      group_top=2, scale=1.5)
+            ids, w = check(x, K, b, **kw)
+            ids2, w2 = route(many, K, b, **kw)
+            assert np.array_equal(ids2, np.tile(ids, (220, 1))[:32797])
+            # other lanes add the weights' sum in another order
+            assert np.allclose(w2, np.tile(w, (220, 1))[:32797], rtol=2 * 64 * U, atol=0)
 
 
 def test_route_many_tokens_repeat_bitwise_and_independent_of_the_batch():
