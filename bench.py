@@ -46,7 +46,7 @@ sys.path.insert(0, ROOT)
 METRIC = "fused reduce+RMSNorm GB/s and % of GB300 HBM peak; tokens/s at T=1K–16K"
 PLANNER_SMS = 148  # SMs the planner models for the compute kernels (split workload)
 FALLBACK_HBM_GBS = 6800.0
-KERNEL_SRC = os.path.join(ROOT, "reduce_rmsnorm_gb300", "csrc", "fused_kernel.cu")
+KERNEL_SRC = os.path.join(ROOT, "reduce_rmsnorm_gb300", "csrc", "fused_forms.cuh")
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "fused_kernel_traffic.json")
 
 

@@ -25,8 +25,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build", "libtw")
 LIB = os.path.join(PKG, "libtw.so")
 
-SOURCES = ["fused_kernel.cu", "combine_kernel.cu", "route_kernel.cu", "unfused_kernels.cu", "abi.cpp",
-           "planner.cpp"]
+SOURCES = ["fused_kernel.cu", "fused_q8_kernel.cu", "combine_kernel.cu", "route_kernel.cu",
+           "unfused_kernels.cu", "abi.cpp", "planner.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2,-fvisibility=hidden",
               "-I", INCLUDE, "-I", CSRC] + ARCH

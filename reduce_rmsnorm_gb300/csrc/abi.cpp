@@ -64,6 +64,9 @@ int validate(const void* const* partials, int N, void* residual, const void* gam
   a->eps = eps;
   a->rows = T;
   a->hidden = H;
+  a->scales = nullptr;
+  a->group = 0;
+  a->scale_type = 0;
   return TW_OK;
 }
 
@@ -310,6 +313,11 @@ namespace {
 template <typename P>
 bool aligned_to(const void* p) { return (reinterpret_cast<uintptr_t>(p) & (sizeof(P) - 1)) == 0; }
 
+struct Span {
+  const void* p;
+  int64_t n;  // bytes
+};
+
 // Scale group and type of an e4m3 output; group 0 is the whole row.
 int validate_q8(int64_t H, int group, int scale_type) {
   if (scale_type != TW_SCALE_F32 && scale_type != TW_SCALE_E8M0) return TW_ERR_INVALID_ARG;
@@ -347,7 +355,6 @@ int validate_combine(const void* experts, int64_t M, const int32_t* rows, const 
   // exactly one partial: a row's partials are all read before its output is
   // written, by the CTA that owns the row.
   const int64_t bytes = T * H * 2;
-  struct Span { const void* p; int64_t n; };
   const Span written[3] = {{residual, bytes}, {out, q8 ? T * H : bytes},
                            {scales, q8 ? T * (group ? H / group : 1) *
                                              (scale_type == TW_SCALE_F32 ? 4 : 1) : 0}};
@@ -425,20 +432,41 @@ extern "C" int tw_fused_reduce_residual_rmsnorm_q8(const void* const* partials, 
                                                    int group, int scale_type, tw_stream_t stream,
                                                    int sm_budget) {
   try {
-    if (N < 1 || scale_type < 0) return TW_ERR_INVALID_ARG;
-    // no slot: the dense sum alone; one row index and weight stand in for the
-    // checks of the (unused) slot arrays
-    static const int32_t no_row = -1;
-    static const float no_weight = 0.0f;
-    tw::CombineArgs a;
-    const int st = validate_combine(nullptr, 0, &no_row, &no_weight, 1, partials, N, residual,
-                                    gamma, eps, T, H, out, scales, group, scale_type, sm_budget,
-                                    &a);
+    int st = validate_shape(N, eps, T, H, sm_budget);
+    if (st == TW_OK) st = validate_q8(H, group, scale_type);
     if (st != TW_OK || T == 0) return st;
-    a.k = 0;
-    a.rows = nullptr;
-    a.weights = nullptr;
-    return tw::launch_combine(a, reinterpret_cast<cudaStream_t>(stream), sm_budget);
+    if (!partials || !residual || !gamma || !out || !scales) return TW_ERR_INVALID_ARG;
+    for (int r = 0; r < N; ++r)
+      if (!partials[r]) return TW_ERR_INVALID_ARG;
+    for (int r = 0; r < N; ++r)
+      if (!aligned16(partials[r])) return TW_ERR_ALIGN;
+    if (!aligned16(residual) || !aligned16(gamma) || !aligned_to<int64_t>(out)) return TW_ERR_ALIGN;
+    if (scale_type == TW_SCALE_F32 && !aligned_to<float>(scales)) return TW_ERR_ALIGN;
+    // the written tensors overlap nothing else
+    const int64_t bytes = T * H * 2;
+    const Span written[3] = {{residual, bytes}, {out, T * H},
+                             {scales, T * (group ? H / group : 1) * (scale_type == TW_SCALE_F32 ? 4 : 1)}};
+    for (int i = 0; i < 3; ++i) {
+      const Span& w = written[i];
+      for (int j = 0; j < i; ++j)
+        if (overlap(w.p, w.n, written[j].p, written[j].n)) return TW_ERR_INVALID_ARG;
+      if (overlap(w.p, w.n, gamma, H * 2)) return TW_ERR_INVALID_ARG;
+      for (int r = 0; r < N; ++r)
+        if (overlap(w.p, w.n, partials[r], bytes)) return TW_ERR_INVALID_ARG;
+    }
+    tw::FusedArgs a;
+    for (int r = 0; r < N; ++r) a.partials[r] = partials[r];
+    a.n = N;
+    a.residual = residual;
+    a.gamma = gamma;
+    a.out = out;
+    a.eps = eps;
+    a.rows = T;
+    a.hidden = H;
+    a.scales = scales;
+    a.group = static_cast<int>(group ? group : H);
+    a.scale_type = scale_type;
+    return tw::launch_fused_q8(a, reinterpret_cast<cudaStream_t>(stream), sm_budget);
   } catch (...) {
     return TW_ERR_CUDA;
   }

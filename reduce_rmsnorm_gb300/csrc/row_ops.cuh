@@ -1,4 +1,4 @@
-// Device helpers shared by the row kernels (fused_kernel.cu, combine_kernel.cu):
+// Device helpers shared by the row kernels (fused_forms.cuh, combine_kernel.cu):
 // programmatic dependent launch, the L2 prefetch hint, bf16 vectors of 8 and
 // the e4m3 output with its scales.
 #pragma once

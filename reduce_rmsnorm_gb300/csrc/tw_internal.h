@@ -20,6 +20,10 @@ struct FusedArgs {
   float eps;
   int64_t rows;
   int64_t hidden;
+  // e4m3 output only
+  void* scales;
+  int group;  // values per scale (H for a whole row)
+  int scale_type;
 };
 
 struct LaunchShape {
@@ -35,6 +39,8 @@ int plan_launch(int64_t rows, int64_t hidden, int n, int sm_budget, LaunchShape*
 
 // Enqueue the fused kernel on `stream`. smid_out: optional device int32[grid].
 int launch_fused(const FusedArgs& a, cudaStream_t stream, int sm_budget, int* smid_out);
+// The same with an e4m3 output and scales.
+int launch_fused_q8(const FusedArgs& a, cudaStream_t stream, int sm_budget);
 
 // Unfused baseline (unfused_kernels.cu): S = bf16(sum of partials), then the
 // residual add + RMSNorm of the stored residual.
@@ -64,8 +70,9 @@ struct CombineArgs {
   int64_t hidden;
 };
 int launch_combine(const CombineArgs& a, cudaStream_t stream, int sm_budget);
-// Read (and optionally clear) the combine kernels' device-side error word,
-// after the device was synchronised.
+// Read (and optionally clear) the device-side error words of the 8-bit step's
+// and the combine kernels, after the device was synchronised.
+int read_fused_q8_error(int reset, unsigned* code);
 int read_combine_error(int reset, unsigned* code);
 
 // Arguments of one routing launch, already validated.
