@@ -63,6 +63,7 @@
 #include <cstdint>
 #include <mutex>
 
+#include "ring_ops.cuh"
 #include "row_ops.cuh"
 #include "tw_internal.h"
 
@@ -70,22 +71,11 @@ namespace tw {
 
 namespace {
 
-// Device-side error word of the kernels of this translation unit (bit 0:
-// consumer wait, bit 1: producer wait, bit 2: final drain).
-__device__ unsigned int g_device_error = 0;
-
-constexpr int kConsumerWarps = 8;
-constexpr int kConsumerThreads = kConsumerWarps * 32;
 // A "slot" is one 16-byte vector per consumer thread: 256 vectors, 4 KiB of a
 // source row. A chunk (the unit of one bulk copy per source) is VPT slots.
 constexpr int kSlotVec = kConsumerThreads;
 constexpr int kSlotBytes = kSlotVec * 16;
-constexpr int kMaxStages = 32;
-constexpr int kConsumerBarrierId = 1;            // named barrier of the consumer warps
 
-constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // give up after 2 s
-constexpr uint32_t kWaitLimitPolls = 1u << 26;
-constexpr unsigned long long kDrainLimitNs = 200000000ull;  // 0.2 s per stage
 // L2 warm-up before the dependency wait: bytes per CTA over all sources, and
 // the size of one prefetch instruction. Measured on T = 512-8192, H = 4096-16384,
 // N = 2-16: best or within 1% of the best of 4-24 KiB per source.
@@ -115,132 +105,6 @@ struct Params {
   float eps;
   float hidden;
 };
-
-// ------------------------------------------------------------------ PTX helpers
-
-__device__ __forceinline__ uint32_t smem_addr(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
-__device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(count)
-               : "memory");
-}
-
-__device__ __forceinline__ void fence_mbar_init() {
-  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)),
-               "r"(bytes)
-               : "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
-}
-
-__device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(smem_addr(bar)), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-
-__device__ __forceinline__ unsigned long long global_timer_ns() {
-  unsigned long long t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-
-__device__ __forceinline__ uint64_t l2_evict_first_policy() {
-  uint64_t pol;
-  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
-  return pol;
-}
-
-__device__ __forceinline__ uint64_t l2_evict_normal_policy() {
-  uint64_t pol;
-  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
-  return pol;
-}
-
-// 1-D TMA bulk copy global -> shared, completing `bytes` on the mbarrier.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar,
-                                          uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1], %2, [%3], %4;" ::"r"(smem_addr(dst)),
-      "l"(src), "r"(bytes), "r"(smem_addr(bar)), "l"(policy)
-      : "memory");
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr));
-  return v;
-}
-
-__device__ __forceinline__ uint32_t sm_id() {
-  uint32_t id;
-  asm volatile("mov.u32 %0, %%smid;" : "=r"(id));
-  return id;
-}
-
-// Wait for the phase of the given parity of *bar to complete. Bounded: gives
-// up after limit_ns (kWaitLimitNs in the kernels) or kWaitLimitPolls polls,
-// then sets *abort and the device error word. Returns false at once while
-// *abort is set.
-__device__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned code,
-                           unsigned long long limit_ns = kWaitLimitNs) {
-  if (*abort) return false;
-  if (mbar_try_wait(bar, parity)) return true;
-  const unsigned long long t0 = global_timer_ns();
-  for (uint32_t i = 1; i < kWaitLimitPolls; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 255u) == 0u) {
-      if (*abort) return false;
-      if (global_timer_ns() - t0 > limit_ns) break;
-    }
-  }
-  *abort = 1;
-  atomicOr(&g_device_error, code);
-  return false;
-}
-
-// Bounded wait that ignores the abort flag (used to drain in-flight copies).
-__device__ bool drain_phase(uint64_t* bar, uint32_t parity) {
-  const unsigned long long t0 = global_timer_ns();
-  for (uint32_t i = 0; i < kWaitLimitPolls; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 255u) == 255u && global_timer_ns() - t0 > kDrainLimitNs) break;
-  }
-  atomicOr(&g_device_error, 4u);
-  return false;
-}
-
-// Waits (bounded) until every bulk copy a producer issued into its ring of
-// `stages` stages has landed: `issued` items went out in order, item i on
-// stage i % stages in phase i / stages, so the last item of each stage
-// completes after all earlier ones there. The producer owns this drain, on
-// the normal path too (where it returns as the consumers' waits complete),
-// so no CTA exits with copies into its shared memory in flight, even if a
-// consumer gives up a wait after the producer has left its issue loop.
-__device__ void drain_ring(uint64_t* full, int stages, long long issued) {
-  const long long last = issued - 1;
-  for (int st = 0; st < stages && st <= last; ++st) {
-    const long long it_last = last - ((last - st) % stages);
-    drain_phase(&full[st], static_cast<uint32_t>((it_last / stages) & 1));
-  }
-}
 
 // ------------------------------------------------------------------ the kernel
 
@@ -279,101 +143,6 @@ __device__ __forceinline__ void reduce_vector(uint32_t src, uint32_t cbytes, int
       add8(q0, a); add8(q1, a);
     } else if (left == 1) {
       add8(lds128(src + r * cbytes), a);
-    }
-  }
-}
-
-// The end of a row, shared by every kernel form: the sum of squares is
-// reduced across the warp (xor shuffle) and then across the pipeline's 8
-// warps in warp order (through `wsum`, this row's 8 floats), r = rsqrt(mean +
-// eps), and Y = (z * r) * gamma is stored as bf16. With evict-first loads the
-// output is stored streaming too, so its lines drain during this launch; with
-// normal loads the store policy measured within 0.2%. A kernel that reads Y
-// right after still finds it unless L2 needs the room. The residual keeps the
-// default policy (evict-first there measured -1%).
-//
-// Q8: a group's largest |y| comes from an xor shuffle, since its group / 8
-// vectors lie in adjacent lanes of one warp and slot. One scale for the row
-// needs no second barrier: max |z gamma| is reduced beside the sum of squares
-// (`wmax`), and r times it is max |y| up to the products' roundings (2^-23,
-// against the codes' 2^-4).
-template <int KMAX, bool EXACT, bool Q8, int GN>
-__device__ __forceinline__ void finish_row(const Params& p, float ss, const float (&z)[KMAX][8],
-                                           const uint4 (&g_reg)[GN], float* wsum, float* wmax,
-                                           int bar_id, int lane, int wg, int t, int vpr,
-                                           long long row) {
-  const bool row_scale = Q8 && p.group == 8 * vpr;
-  float am = 0.0f;
-  if constexpr (Q8) {
-    if (row_scale) {
-#pragma unroll
-      for (int j = 0; j < KMAX; ++j) {
-        const int v = j * kSlotVec + t;
-        if (EXACT || v < vpr) {
-          float y[8];
-          if constexpr (GN == KMAX) scale8(z[j], 1.0f, g_reg[j], y);
-          else scale8(z[j], 1.0f, __ldg(p.gamma + v), y);
-          am = fmaxf(am, amax8(y));
-        }
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-    }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  if (lane == 0) {
-    wsum[wg] = ss;
-    if constexpr (Q8) wmax[wg] = am;
-  }
-  asm volatile("bar.sync %0, %1;" ::"r"(bar_id), "n"(kConsumerThreads) : "memory");
-  const float total = warp_total(wsum);
-  const float rs = rsqrtf(total / p.hidden + p.eps);
-  if constexpr (Q8) {
-    uint2* out_row = static_cast<uint2*>(p.out) + row * vpr;
-    GroupScale gs = {};
-    if (row_scale) {
-      const float4 a = *reinterpret_cast<const float4*>(wmax);
-      const float4 b = *reinterpret_cast<const float4*>(wmax + 4);
-      am = fmaxf(fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)), fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w)));
-      gs = group_scale(am * rs, p.scale_type);
-      if (t == 0) store_scale(p.scales, row, gs, p.scale_type);
-    }
-    const int per = p.group >> 3;  // vectors per group
-#pragma unroll
-    for (int j = 0; j < KMAX; ++j) {
-      const int v = j * kSlotVec + t;
-      const bool in = EXACT || v < vpr;
-      float y[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-      if (in) {
-        if constexpr (GN == KMAX) scale8(z[j], rs, g_reg[j], y);
-        else scale8(z[j], rs, __ldg(p.gamma + v), y);
-      }
-      if (!row_scale) {
-        float a = amax8(y);
-        for (int o = per >> 1; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-        gs = group_scale(a, p.scale_type);
-        if (in && (v & (per - 1)) == 0)
-          store_scale(p.scales, (row * vpr + v) / per, gs, p.scale_type);
-      }
-      if (in) {
-        const uint2 q = pack_e4m3(y, gs.inv);
-        if (p.l2_stream) __stcs(out_row + v, q);
-        else out_row[v] = q;
-      }
-    }
-  } else {
-    uint4* out_row = static_cast<uint4*>(p.out) + row * vpr;
-#pragma unroll
-    for (int j = 0; j < KMAX; ++j) {
-      const int v = j * kSlotVec + t;
-      if (EXACT || v < vpr) {
-        float y[8];
-        if constexpr (GN == KMAX) scale8(z[j], rs, g_reg[j], y);
-        else scale8(z[j], rs, __ldg(p.gamma + v), y);
-        if (p.l2_stream) __stcs(out_row + v, pack8(y));
-        else out_row[v] = pack8(y);
-      }
     }
   }
 }
@@ -568,8 +337,8 @@ __global__ void __launch_bounds__(G * kConsumerThreads + 32, 1)
     // the two row buffers of warp sums alternate, so a warp can post row i + 1
     // while slower warps still read row i's
     finish_row<KMAX, EXACT, Q8>(p, ss, z, g_reg, warp_ss[g][(row - ra) & 1],
-                                warp_max[Q8 ? g : 0][(row - ra) & 1], kConsumerBarrierId + g, lane,
-                                wg, t, vpr, row);
+                                warp_max[Q8 ? g : 0][(row - ra) & 1], kConsumerBarrierId + g,
+                                kConsumerThreads, lane, wg, t, vpr, row);
   }
 }
 
@@ -647,8 +416,8 @@ __global__ void __launch_bounds__(kConsumerThreads, 1)
       res_row[v] = pack8(z[j]);
     }
   }
-  finish_row<KMAX, EXACT, Q8>(p, ss, z, g_reg, warp_ss, warp_max, kConsumerBarrierId, lane, wg, t,
-                              vpr, row);
+  finish_row<KMAX, EXACT, Q8>(p, ss, z, g_reg, warp_ss, warp_max, kConsumerBarrierId,
+                              kConsumerThreads, lane, wg, t, vpr, row);
 }
 
 // Row-ring form: one bulk copy per (row, source), so a stage holds one
@@ -814,8 +583,8 @@ __global__ void __launch_bounds__(G * kConsumerThreads + 32, 1)
       }
     }
     finish_row<KMAX, EXACT, Q8>(p, ss, z, g_reg, warp_ss[g][(row - ra) & 1],
-                                warp_max[Q8 ? g : 0][(row - ra) & 1], kConsumerBarrierId + g, lane,
-                                wg, t, vpr, row);
+                                warp_max[Q8 ? g : 0][(row - ra) & 1], kConsumerBarrierId + g,
+                                kConsumerThreads, lane, wg, t, vpr, row);
   }
 }
 
@@ -1240,15 +1009,6 @@ int launch_forms(const FusedArgs& a, cudaStream_t stream, int sm_budget, int* sm
   if (cudaLaunchKernelEx(&cfg, fn, p) != cudaSuccess) {
     cudaGetLastError();
     return TW_ERR_CUDA;
-  }
-  return TW_OK;
-}
-
-int read_forms_error(int reset, unsigned* code) {
-  if (cudaMemcpyFromSymbol(code, g_device_error, sizeof(*code)) != cudaSuccess) return TW_ERR_CUDA;
-  if (reset && *code) {
-    const unsigned zero = 0;
-    if (cudaMemcpyToSymbol(g_device_error, &zero, sizeof(zero)) != cudaSuccess) return TW_ERR_CUDA;
   }
   return TW_OK;
 }

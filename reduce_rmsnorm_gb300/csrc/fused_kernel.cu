@@ -43,7 +43,7 @@ int launch_wait_probe(long long limit_ns, cudaStream_t stream) {
 int read_device_error(int reset, int* code) {
   if (cudaDeviceSynchronize() != cudaSuccess) return TW_ERR_CUDA;
   unsigned fused = 0, q8 = 0, combine = 0;
-  int st = read_forms_error(reset, &fused);
+  int st = read_ring_error(reset, &fused);
   if (st == TW_OK) st = read_fused_q8_error(reset, &q8);
   if (st == TW_OK) st = read_combine_error(reset, &combine);
   if (st != TW_OK) return st;

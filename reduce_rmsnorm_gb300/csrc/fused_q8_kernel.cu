@@ -9,6 +9,6 @@ int launch_fused_q8(const FusedArgs& a, cudaStream_t stream, int sm_budget) {
   return launch_forms(a, stream, sm_budget, nullptr);
 }
 
-int read_fused_q8_error(int reset, unsigned* code) { return read_forms_error(reset, code); }
+int read_fused_q8_error(int reset, unsigned* code) { return read_ring_error(reset, code); }
 
 }  // namespace tw

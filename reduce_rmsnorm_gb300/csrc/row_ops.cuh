@@ -1,6 +1,6 @@
 // Device helpers shared by the row kernels (fused_forms.cuh, combine_kernel.cu):
-// programmatic dependent launch, the L2 prefetch hint, bf16 vectors of 8 and
-// the e4m3 output with its scales.
+// programmatic dependent launch, the L2 prefetch hint, bf16 vectors of 8, the
+// e4m3 output with its scales and the end of a row.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -127,6 +127,8 @@ __device__ __forceinline__ GroupScale group_scale(float amax, int scale_type) {
     g.inv = inf ? 0.0f : __uint_as_float((254u - g.code) << 23);  // code <= 247
     g.scale = 0.0f;
   } else {
+    // IEEE divisions: a product and an approximate reciprocal in their place
+    // made the longest rows slower (T = 8192, H = 16384, N = 8 400 -> 418 us)
     g.scale = fmaxf(amax / kE4m3Max, kScaleMin);
     g.inv = 1.0f / g.scale;
     g.code = 0u;
@@ -163,6 +165,127 @@ __device__ __forceinline__ float amax8(const float y[8]) {
 #pragma unroll
   for (int i = 1; i < 8; ++i) m = fmaxf(m, fabsf(y[i]));
   return m;
+}
+
+// ------------------------------------------------------------------ the end of a row
+
+constexpr int kConsumerWarps = 8;  // of a pipeline
+constexpr int kConsumerThreads = kConsumerWarps * 32;
+constexpr int kConsumerBarrierId = 1;            // named barrier of the consumer warps
+
+// The end of a row, shared by every kernel form: the sum of squares is
+// reduced across the warp (xor shuffle) and then across the pipeline's 8
+// warps in warp order (through `wsum`, this row's 8 floats), r = rsqrt(mean +
+// eps), and Y = (z * r) * gamma is stored as bf16. With evict-first loads the
+// output is stored streaming too, so its lines drain during this launch; with
+// normal loads the store policy measured within 0.2%. A kernel that reads Y
+// right after still finds it unless L2 needs the room. The residual keeps the
+// default policy (evict-first there measured -1%).
+//
+// Q8: a group's largest |y| comes from an xor shuffle, since its group / 8
+// vectors lie in adjacent lanes of one warp and slot. One scale for the row
+// needs no second barrier: max |z gamma| is reduced beside the sum of squares
+// (`wmax`), and r times it is max |y| up to the products' roundings (2^-23,
+// against the codes' 2^-4).
+//
+// Thread t of `threads` (a multiple of 32, at most 256) owns the vectors t, t +
+// threads, ...: slot j is vector j * threads + t. With fewer than 8 warps the
+// others' wsum and wmax are 0.
+template <int KMAX, bool EXACT, bool Q8, int GN, typename P>
+__device__ __forceinline__ void finish_row(const P& p, float ss, const float (&z)[KMAX][8],
+                                           const uint4 (&g_reg)[GN], float* wsum, float* wmax,
+                                           int bar_id, int threads, int lane, int wg, int t,
+                                           int vpr, long long row) {
+  const bool row_scale = Q8 && p.group == 8 * vpr;
+  float am = 0.0f;
+  if constexpr (Q8) {
+    if (row_scale) {
+#pragma unroll
+      for (int j = 0; j < KMAX; ++j) {
+        const int v = j * threads + t;
+        if (EXACT || v < vpr) {
+          float y[8];
+          if constexpr (GN == KMAX) scale8(z[j], 1.0f, g_reg[j], y);
+          else scale8(z[j], 1.0f, __ldg(p.gamma + v), y);
+          am = fmaxf(am, amax8(y));
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  if (lane == 0) {
+    wsum[wg] = ss;
+    if constexpr (Q8) wmax[wg] = am;
+  }
+  asm volatile("bar.sync %0, %1;" ::"r"(bar_id), "r"(threads) : "memory");
+  const float total = warp_total(wsum);
+  const float rs = rsqrtf(total / p.hidden + p.eps);
+  if constexpr (Q8) {
+    uint2* out_row = static_cast<uint2*>(p.out) + row * vpr;
+    GroupScale gs = {};
+    if (row_scale) {
+      const float4 a = *reinterpret_cast<const float4*>(wmax);
+      const float4 b = *reinterpret_cast<const float4*>(wmax + 4);
+      am = fmaxf(fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)), fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w)));
+      gs = group_scale(am * rs, p.scale_type);
+      if (t == 0) store_scale(p.scales, row, gs, p.scale_type);
+    }
+    const int per = p.group >> 3;  // vectors per group
+    // a few slots at a time, so that their shuffles overlap: T = 8192, H =
+    // 16384, N = 8 takes 404 us with one slot at a time, 400 with two, 418 with
+    // four
+    constexpr int B = KMAX <= 4 ? KMAX : 2;
+#pragma unroll
+    for (int j0 = 0; j0 < KMAX; j0 += B) {
+      float y[B][8], a[B];
+#pragma unroll
+      for (int u = 0; u < B; ++u) {
+        const int j = j0 + u, v = j * threads + t;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[u][i] = 0.0f;
+        if (EXACT || v < vpr) {
+          if constexpr (GN == KMAX) scale8(z[j], rs, g_reg[j], y[u]);
+          else scale8(z[j], rs, __ldg(p.gamma + v), y[u]);
+        }
+        a[u] = amax8(y[u]);
+      }
+      if (!row_scale) {
+        for (int o = per >> 1; o > 0; o >>= 1)
+#pragma unroll
+          for (int u = 0; u < B; ++u) a[u] = fmaxf(a[u], __shfl_xor_sync(0xffffffffu, a[u], o));
+      }
+#pragma unroll
+      for (int u = 0; u < B; ++u) {
+        const int v = (j0 + u) * threads + t;
+        if (EXACT || v < vpr) {
+          if (!row_scale) {
+            gs = group_scale(a[u], p.scale_type);
+            if ((v & (per - 1)) == 0)
+              store_scale(p.scales, (row * vpr + v) / per, gs, p.scale_type);
+          }
+          const uint2 q = pack_e4m3(y[u], gs.inv);
+          if (p.l2_stream) __stcs(out_row + v, q);
+          else out_row[v] = q;
+        }
+      }
+    }
+  } else {
+    uint4* out_row = static_cast<uint4*>(p.out) + row * vpr;
+#pragma unroll
+    for (int j = 0; j < KMAX; ++j) {
+      const int v = j * threads + t;
+      if (EXACT || v < vpr) {
+        float y[8];
+        if constexpr (GN == KMAX) scale8(z[j], rs, g_reg[j], y);
+        else scale8(z[j], rs, __ldg(p.gamma + v), y);
+        if (p.l2_stream) __stcs(out_row + v, pack8(y));
+        else out_row[v] = pack8(y);
+      }
+    }
+  }
 }
 
 }  // namespace
