@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kConsumerThreads)
 #pragma unroll
     for (int j = 0; j < KMAX; ++j)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) z[j][i] = 0.0f;
+      for (int i = 0; i < 8; ++i) z[j][i] = -0.0f;  // -0 + x is x, -0 too
     // the kept slots in order, U at a time
     for (unsigned left = kept_slots(p, slot, warp == 0); left != 0u;) {
       uint4 q[U][KMAX];
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kConsumerThreads + 32, 1)
 #pragma unroll
         for (int u = 0; u < VPT; ++u)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) z[c * VPT + u][i] = 0.0f;
+          for (int i = 0; i < 8; ++i) z[c * VPT + u][i] = -0.0f;  // -0 + x is x, -0 too
         // four sources at a time, then the one to three left
         int i = 0;
         for (; i + 3 < sources; i += 4) {
@@ -529,6 +529,7 @@ int launch_combine(const CombineArgs& a, cudaStream_t stream, int sm_budget) {
   while ((kConsumerThreads << kc) < p.vec_per_row) ++kc;
   const int kmax = 1 << kc;
   p.threads = ((p.vec_per_row + kmax - 1) / kmax + 31) / 32 * 32;
+  if (a.k == 0 && kmax > 1) p.threads = kConsumerThreads;  // the fused step's layout
   const int q8 = a.scale_type >= 0 ? 1 : 0;
   int64_t grid = d->sms;
   if (sm_budget > 0 && sm_budget < grid) grid = sm_budget;

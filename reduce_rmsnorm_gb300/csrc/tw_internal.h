@@ -50,7 +50,9 @@ int launch_add_rmsnorm(const void* sum, void* residual, const void* gamma, float
                        int64_t hidden, void* out, cudaStream_t stream);
 
 // Arguments of one combine launch, already validated. scale_type < 0: bf16
-// output; otherwise e4m3 with scales.
+// output; otherwise e4m3 with scales. k == 0 (with n >= 1): the dense step, its
+// vectors given to threads as in the fused step's kernels, so that the rows are
+// bitwise theirs.
 struct CombineArgs {
   const void* experts;
   int64_t m;
