@@ -43,11 +43,16 @@ constexpr int kRouteBlocks = 152 * 12;  // about what is resident at once; large
 // From this many tokens on, rows of 65 to 256 experts share a warp four by
 // four, which halves the instructions per row but has four rows wait for one
 // that is settled in fp64. Measured against one row per warp (256 experts, K =
-// 8): no bias 3.1 against 3.1 us at 2048 tokens, 3.8 / 4.1 at 4096, 8.6 / 11.1
-// at 16384; sigmoid with bias and groups 12.5 / 7.8 at 4096, 21.2 / 19.6 at
-// 16384, 32.4 / 33.6 at 32768.
+// 8): bf16, no bias 3.0 against 3.1 us at 2048 tokens, 3.5 / 4.1 at 4096, 7.5 /
+// 11.1 at 16384; sigmoid with bias and groups 11.2 / 7.8 at 4096, 14.3 / 11.7 at
+// 8192, 17.9 / 19.6 at 16384, 27.1 / 33.6 at 32768.
 constexpr int64_t kLongTokens = 4096;
-constexpr int64_t kLongTokensByValue = 32768;
+constexpr int64_t kLongTokensByValue = 12288;
+// Resident blocks per SM that the 32 fp32 values of a lane leave registers for
+// (168 registers, three blocks, without a bound: 256 experts, sigmoid + bias +
+// groups 18.8 against 17.9 us at 16384 tokens, 29.6 / 27.1 at 32768; a bound
+// for the others made them slower).
+constexpr int kBlocks32 = 5;
 constexpr unsigned kAll = 0xffffffffu;
 constexpr uint32_t kNone = 1024u;          // fixed-point keys below: no candidate
 constexpr uint32_t kNone16 = 0x00800000u;  // the same for keys of bf16 logits
@@ -121,6 +126,55 @@ __device__ __forceinline__ void load_row(const RouteParams& p, long long row, in
       x[i] = there && e0 + i < p.experts ? load_logit<BF16>(p, row, e0 + i) : -INFINITY;
   }
 }
+
+// The same for the 4 rows of a warp with 8 lanes each, through shared memory:
+// the rows are one run of bytes, read 512 at a time by the whole warp; a lane
+// then takes its C 16-byte pieces in an order that depends on the lane (order()),
+// so that 8 lanes read from all banks. Straight from global memory every lane
+// would touch a line of its own in every load, 8 times the L1 wavefronts. The
+// order of a lane's values does not matter: keys carry the index.
+template <int V, bool BF16>
+struct Staged {
+  static constexpr int kPer = BF16 ? 8 : 4;  // values per piece
+  static constexpr int C = V / kPer;         // pieces per lane
+  static __device__ __forceinline__ int order(int sub, int i) { return i ^ ((sub * C / 8) & (C - 1)); }
+  // the expert of a lane's i-th value
+  static __device__ __forceinline__ int expert(int sub, int i) {
+    return sub * V + order(sub, i / kPer) * kPer + i % kPer;
+  }
+  static __device__ __forceinline__ void load(const RouteParams& p, long long first, int rows,
+                                              int lane, bool there, uint4* stage, float (&x)[V]) {
+    const int row_pieces = p.experts / kPer;
+    const uint4* from = reinterpret_cast<const uint4*>(
+        static_cast<const char*>(p.logits) + first * row_pieces * 16);
+    const int all = rows * row_pieces;
+    uint4 q[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) q[i] = i * 32 + lane < all ? __ldg(from + i * 32 + lane) : uint4{};
+    __syncwarp();  // the last rows have been read
+#pragma unroll
+    for (int i = 0; i < C; ++i) stage[i * 32 + lane] = q[i];
+    __syncwarp();
+    const int sub = lane & 7;
+    there = there && sub * V < p.experts;
+    const uint32_t out = BF16 ? 0xff80ff80u : 0xff800000u;  // -inf
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const uint4 v = there ? stage[(lane >> 3) * row_pieces + sub * C + order(sub, i)]
+                            : make_uint4(out, out, out, out);
+      if constexpr (BF16) {
+        load8(v, &x[8 * i]);
+      } else {
+        x[4 * i] = __uint_as_float(v.x);
+        x[4 * i + 1] = __uint_as_float(v.y);
+        x[4 * i + 2] = __uint_as_float(v.z);
+        x[4 * i + 3] = __uint_as_float(v.w);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = clean(x[i]);
+  }
+};
 
 // ------------------------------------------------------------------ across lanes
 //
@@ -884,7 +938,7 @@ __device__ __forceinline__ void merge_lanes(uint32_t (&k)[8], uint32_t& next) {
 // instructions a level, for all rows of the warp at once); otherwise (V = 8)
 // K rounds of a maximum over the lanes' first keys.
 template <int V, int L, bool SMALLK, bool SIGMOID, bool BF16, bool VEC>
-__global__ void __launch_bounds__(kRouteWarps * 32)
+__global__ void __launch_bounds__(kRouteWarps * 32, V == 32 && !BF16 ? kBlocks32 : 1)
     route_rows_kernel(const __grid_constant__ RouteParams p) {
   static_assert(V == 8 || SMALLK, "longer lists keep their 8 largest keys");
   constexpr int kRows = 32 / L;  // rows of a warp
@@ -903,9 +957,28 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
   const bool check = !(BF16 && !biased);  // bf16 logits have exact keys
   const uint32_t none = check ? kNone : kNone16;
   const int per = p.group_size / V;  // lanes per group
-  float bias[V];
+  // Longer lists come through shared memory, as their biases do (padded, so
+  // that 8 lanes read from all banks); 8 biases stay in registers.
+  constexpr bool kStaged = V > 8;
+  using Stage = Staged<V, BF16>;
+  __shared__ __align__(16) uint4 s_stage[kStaged ? kRouteWarps : 1][kStaged ? 32 * Stage::C : 1];
+  __shared__ __align__(16) float s_bias[kStaged ? L * (V + 4) : 1];
+  float bias[kStaged ? 1 : V];
+  if constexpr (kStaged) {
+    if (biased) {
+      for (int e = threadIdx.x; e < p.experts; e += kRouteWarps * 32)
+        s_bias[e / V * (V + 4) + e % V] = load_bias(p, e);
+      __syncthreads();
+    }
+  } else {
 #pragma unroll
-  for (int i = 0; i < V; ++i) bias[i] = biased && e0 + i < p.experts ? load_bias(p, e0 + i) : 0.0f;
+    for (int i = 0; i < V; ++i) bias[i] = biased && e0 + i < p.experts ? load_bias(p, e0 + i) : 0.0f;
+  }
+  // the expert of the lane's i-th value
+  auto expert = [&](int i) {
+    if constexpr (kStaged) return Stage::expert(sub, i);
+    else return e0 + i;
+  };
   const long long stride = static_cast<long long>(gridDim.x) * kRouteWarps * kRows;
   for (long long first = (static_cast<long long>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5)) *
                          kRows;
@@ -913,7 +986,13 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
     const long long row = first + lane / L;
     const bool there = row < p.tokens;
     float c[V];
-    load_row<V, BF16, VEC>(p, row, e0, there, c);
+    if constexpr (kStaged) {
+      const long long rows = p.tokens - first;
+      Stage::load(p, first, rows < kRows ? static_cast<int>(rows) : kRows, lane, there,
+                  s_stage[threadIdx.x >> 5], c);
+    } else {
+      load_row<V, BF16, VEC>(p, row, e0, there, c);
+    }
     float top = 0.0f, total = 1.0f, inv_total = 1.0f;
     if (!SIGMOID && (by_value || !p.renormalize)) {
       softmax_stats<V, L>(c, top, total);
@@ -921,8 +1000,23 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
     }
     const float largest = SIGMOID ? 1.0f : inv_total;
     if (biased) {
+      if constexpr (kStaged) {
+        // four at a time: a piece holds 4 or 8
 #pragma unroll
-      for (int i = 0; i < V; ++i) c[i] = value_of<SIGMOID>(c[i], bias[i], top, inv_total);
+        for (int i = 0; i < V; i += 4) {
+          const float4 b =
+              sub * V < p.experts
+                  ? *reinterpret_cast<const float4*>(&s_bias[sub * (V + 4) + expert(i) % V])
+                  : float4{};
+          c[i] = value_of<SIGMOID>(c[i], b.x, top, inv_total);
+          c[i + 1] = value_of<SIGMOID>(c[i + 1], b.y, top, inv_total);
+          c[i + 2] = value_of<SIGMOID>(c[i + 2], b.z, top, inv_total);
+          c[i + 3] = value_of<SIGMOID>(c[i + 3], b.w, top, inv_total);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) c[i] = value_of<SIGMOID>(c[i], bias[i], top, inv_total);
+      }
     }
     bool stays = true;  // this lane's group
     if (L > 1 && grouped) {
@@ -994,13 +1088,14 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
 #pragma unroll
     for (int v = 0; v < V; v += 8) {
       uint32_t part[8];
-      const uint32_t tail = 1023u - static_cast<uint32_t>(e0 + v);
       if (check) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) part[i] = fixed_key(c[v + i], f, tail - i);
+        for (int i = 0; i < 8; ++i)
+          part[i] = fixed_key(c[v + i], f, 1023u - static_cast<uint32_t>(expert(v + i)));
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) part[i] = stays ? bf16_key(c[v + i], tail - i) : 0u;
+        for (int i = 0; i < 8; ++i)
+          part[i] = stays ? bf16_key(c[v + i], 1023u - static_cast<uint32_t>(expert(v + i))) : 0u;
       }
       sort_descending<8>(part);
       if (v == 0) {
