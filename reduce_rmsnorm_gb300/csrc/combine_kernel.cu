@@ -149,9 +149,7 @@ __global__ void __launch_bounds__(kConsumerThreads)
   __syncthreads();
   grid_dependency_wait();
   grid_launch_dependents();
-  // one vector of gamma stays in a register; more are read at the row's end
-  uint4 g_reg[1] = {make_uint4(0, 0, 0, 0)};
-  if (KMAX == 1 && t < vpr) g_reg[0] = __ldg(p.gamma + t);
+  auto gamma = [&](int, int v) { return __ldg(p.gamma + v); };
   int buf = 0;
   for (long long row = blockIdx.x; row < p.tokens; row += gridDim.x, buf ^= 1) {
     const Slot slot = load_slot(p, row, lane);
@@ -223,7 +221,7 @@ __global__ void __launch_bounds__(kConsumerThreads)
     const float ss = square_sum<KMAX, false>(z, t, threads, vpr);
     // The two buffers alternate: a warp writes buffer b for row i + 2 only after
     // row i + 1's barrier, which every warp reaches after it has read b for row i.
-    finish_row<KMAX, false, Q8>(p, ss, z, g_reg, s_sum[buf], s_max[buf], kConsumerBarrierId,
+    finish_row<KMAX, false, Q8>(p, ss, z, gamma, s_sum[buf], s_max[buf], kConsumerBarrierId,
                                 threads, lane, warp, t, vpr, row);
   }
 }
@@ -345,15 +343,24 @@ __global__ void __launch_bounds__(kConsumerThreads + 32, 1)
 
   // ---------------- consumers
   const uint32_t base = smem_addr(ring) + static_cast<uint32_t>(tid) * 16u;
-  constexpr bool kGammaRegs = KMAX <= 8;
+  // gamma for the CTA's whole range: in registers, or for long rows in shared
+  // memory behind the ring (with the z of a long row the registers would spill,
+  // and read again from L2 every row it cost 10% at H = 16384)
+  constexpr bool kGammaRegs = KMAX <= 4;
   uint4 g_reg[kGammaRegs ? KMAX : 1];
-  if constexpr (kGammaRegs) {
+  const uint4* s_gamma =
+      reinterpret_cast<const uint4*>(ring + static_cast<size_t>(stages) * stage_bytes);
 #pragma unroll
-    for (int j = 0; j < KMAX; ++j) {
-      const int v = j * threads + tid;
-      g_reg[j] = (EXACT || v < vpr) ? __ldg(p.gamma + v) : make_uint4(0, 0, 0, 0);
-    }
+  for (int j = 0; j < KMAX; ++j) {
+    const int v = j * threads + tid;
+    const uint4 g = (EXACT || v < vpr) ? __ldg(p.gamma + v) : make_uint4(0, 0, 0, 0);
+    if constexpr (kGammaRegs) g_reg[j] = g;
+    else if (EXACT || v < vpr) const_cast<uint4*>(s_gamma)[v] = g;  // read by this thread only
   }
+  auto gamma = [&](int j, int v) {
+    if constexpr (kGammaRegs) return g_reg[j];
+    else return s_gamma[v];
+  };
   int s = 0;
   uint32_t parity = 0;
   float z[KMAX][8];
@@ -424,7 +431,7 @@ __global__ void __launch_bounds__(kConsumerThreads + 32, 1)
         }
       }
     }
-    finish_row<KMAX, EXACT, Q8>(p, ss, z, g_reg, s_sum[row & 1], s_max[row & 1],
+    finish_row<KMAX, EXACT, Q8>(p, ss, z, gamma, s_sum[row & 1], s_max[row & 1],
                                 kConsumerBarrierId, threads, lane, warp, tid, vpr, row);
   }
 }
@@ -529,7 +536,8 @@ int launch_combine(const CombineArgs& a, cudaStream_t stream, int sm_budget) {
   while ((kConsumerThreads << kc) < p.vec_per_row) ++kc;
   const int kmax = 1 << kc;
   p.threads = ((p.vec_per_row + kmax - 1) / kmax + 31) / 32 * 32;
-  if (a.k == 0 && kmax > 1) p.threads = kConsumerThreads;  // the fused step's layout
+  if (kmax >= 8 || (a.k == 0 && kmax > 1))  // a.k == 0: the fused step's layout
+    p.threads = kConsumerThreads;
   const int q8 = a.scale_type >= 0 ? 1 : 0;
   int64_t grid = d->sms;
   if (sm_budget > 0 && sm_budget < grid) grid = sm_budget;
@@ -540,9 +548,10 @@ int launch_combine(const CombineArgs& a, cudaStream_t stream, int sm_budget) {
   // consumers, not HBM, set the pace. As many as the registers hold with at
   // least kMinStages stages each, while each still has a row. An SM budget
   // means one per SM.
+  const int gamma_bytes = kmax > 4 ? p.vec_per_row * 16 : 0;
   int share = sm_budget == 0 ? kMaxShare : 1, vpt2 = 0, stage = 0, stages = 0;
   for (; share >= 1; --share) {
-    const int room = d->smem_optin / share - kStaticSmemReserve;
+    const int room = d->smem_optin / share - kStaticSmemReserve - gamma_bytes;
     // 8 KiB chunks where at least three stages of them fit
     vpt2 = kmax >= 2 && 3 * 2 * chunk * sources <= room ? 1 : 0;
     stage = chunk * (vpt2 + 1) * sources;
@@ -584,7 +593,7 @@ int launch_combine(const CombineArgs& a, cudaStream_t stream, int sm_budget) {
     }
     grid = ring_grid < a.tokens ? ring_grid : a.tokens;
     cfg.blockDim = dim3(static_cast<unsigned>(p.threads + 32));
-    cfg.dynamicSmemBytes = static_cast<size_t>(stages) * stage;
+    cfg.dynamicSmemBytes = static_cast<size_t>(stages) * stage + gamma_bytes;
   } else {
     fn = kDirect[q8][kc];
     if (sm_budget == 0) grid = kMaxGrid;

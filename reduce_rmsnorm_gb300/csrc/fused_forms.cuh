@@ -301,6 +301,10 @@ __global__ void __launch_bounds__(G * kConsumerThreads + 32, 1)
       g_reg[j] = (EXACT || v < vpr) ? __ldg(p.gamma + v) : make_uint4(0, 0, 0, 0);
     }
   }
+  auto gamma = [&](int j, int v) {
+    if constexpr (kGammaRegs) return g_reg[j];
+    else return __ldg(p.gamma + v);
+  };
   int s = 0;
   uint32_t parity = 0;
   float z[KMAX][8];
@@ -336,7 +340,7 @@ __global__ void __launch_bounds__(G * kConsumerThreads + 32, 1)
     }
     // the two row buffers of warp sums alternate, so a warp can post row i + 1
     // while slower warps still read row i's
-    finish_row<KMAX, EXACT, Q8>(p, ss, z, g_reg, warp_ss[g][(row - ra) & 1],
+    finish_row<KMAX, EXACT, Q8>(p, ss, z, gamma, warp_ss[g][(row - ra) & 1],
                                 warp_max[Q8 ? g : 0][(row - ra) & 1], kConsumerBarrierId + g,
                                 kConsumerThreads, lane, wg, t, vpr, row);
   }
@@ -416,7 +420,8 @@ __global__ void __launch_bounds__(kConsumerThreads, 1)
       res_row[v] = pack8(z[j]);
     }
   }
-  finish_row<KMAX, EXACT, Q8>(p, ss, z, g_reg, warp_ss, warp_max, kConsumerBarrierId,
+  auto gamma = [&](int j, int) { return g_reg[j]; };
+  finish_row<KMAX, EXACT, Q8>(p, ss, z, gamma, warp_ss, warp_max, kConsumerBarrierId,
                               kConsumerThreads, lane, wg, t, vpr, row);
 }
 
@@ -536,6 +541,10 @@ __global__ void __launch_bounds__(G * kConsumerThreads + 32, 1)
       g_reg[j] = (EXACT || v < vpr) ? __ldg(p.gamma + v) : make_uint4(0, 0, 0, 0);
     }
   }
+  auto gamma = [&](int j, int v) {
+    if constexpr (kGammaRegs) return g_reg[j];
+    else return __ldg(p.gamma + v);
+  };
   int s = 0;
   uint32_t parity = 0;
   float z[KMAX][8];
@@ -582,7 +591,7 @@ __global__ void __launch_bounds__(G * kConsumerThreads + 32, 1)
         res_row[v] = pack8(z[j]);
       }
     }
-    finish_row<KMAX, EXACT, Q8>(p, ss, z, g_reg, warp_ss[g][(row - ra) & 1],
+    finish_row<KMAX, EXACT, Q8>(p, ss, z, gamma, warp_ss[g][(row - ra) & 1],
                                 warp_max[Q8 ? g : 0][(row - ra) & 1], kConsumerBarrierId + g,
                                 kConsumerThreads, lane, wg, t, vpr, row);
   }

@@ -117,6 +117,9 @@ struct GroupScale {
 // >= a / 448 is 2^(e - 8) for m <= 1.75 and 2^(e - 7) above: an exact rule on
 // a's bits, with no division whose rounding could cross the border. An infinite
 // a has an infinite (fp32) or NaN (e8m0) scale; fmaxf drops a NaN.
+// FAST: a product and an approximate reciprocal, each within an ulp, for the
+// two divisions of an fp32 scale (see finish_row).
+template <bool FAST>
 __device__ __forceinline__ GroupScale group_scale(float amax, int scale_type) {
   GroupScale g;
   if (scale_type == TW_SCALE_E8M0) {
@@ -127,10 +130,9 @@ __device__ __forceinline__ GroupScale group_scale(float amax, int scale_type) {
     g.inv = inf ? 0.0f : __uint_as_float((254u - g.code) << 23);  // code <= 247
     g.scale = 0.0f;
   } else {
-    // IEEE divisions: a product and an approximate reciprocal in their place
-    // made the longest rows slower (T = 8192, H = 16384, N = 8 400 -> 418 us)
-    g.scale = fmaxf(amax / kE4m3Max, kScaleMin);
-    g.inv = 1.0f / g.scale;
+    g.scale = fmaxf(FAST ? amax * (1.0f / kE4m3Max) : amax / kE4m3Max, kScaleMin);
+    if constexpr (FAST) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(g.inv) : "f"(g.scale));
+    else g.inv = 1.0f / g.scale;
     g.code = 0u;
   }
   return g;
@@ -191,11 +193,18 @@ constexpr int kConsumerBarrierId = 1;            // named barrier of the consume
 // Thread t of `threads` (a multiple of 32, at most 256) owns the vectors t, t +
 // threads, ...: slot j is vector j * threads + t. With fewer than 8 warps the
 // others' wsum and wmax are 0.
-template <int KMAX, bool EXACT, bool Q8, int GN, typename P>
+//
+// gamma(j, v): the thread's j-th vector of gamma, which is the row's vector v.
+// Rows of more than 2 vectors a thread that do not fill whole slots take the
+// fast scale (3 to 10% of a combine launch); the others do not, where the
+// largest (T = 8192, H = 16384, N = 8) took 418 us with it and 400 without. The
+// choice depends on H alone, as every bit of a row does.
+template <int KMAX, bool EXACT, bool Q8, typename P, typename Gamma>
 __device__ __forceinline__ void finish_row(const P& p, float ss, const float (&z)[KMAX][8],
-                                           const uint4 (&g_reg)[GN], float* wsum, float* wmax,
+                                           const Gamma& gamma, float* wsum, float* wmax,
                                            int bar_id, int threads, int lane, int wg, int t,
                                            int vpr, long long row) {
+  constexpr bool FAST = KMAX > 2 && !EXACT;
   const bool row_scale = Q8 && p.group == 8 * vpr;
   float am = 0.0f;
   if constexpr (Q8) {
@@ -205,8 +214,7 @@ __device__ __forceinline__ void finish_row(const P& p, float ss, const float (&z
         const int v = j * threads + t;
         if (EXACT || v < vpr) {
           float y[8];
-          if constexpr (GN == KMAX) scale8(z[j], 1.0f, g_reg[j], y);
-          else scale8(z[j], 1.0f, __ldg(p.gamma + v), y);
+          scale8(z[j], 1.0f, gamma(j, v), y);
           am = fmaxf(am, amax8(y));
         }
       }
@@ -230,7 +238,7 @@ __device__ __forceinline__ void finish_row(const P& p, float ss, const float (&z
       const float4 a = *reinterpret_cast<const float4*>(wmax);
       const float4 b = *reinterpret_cast<const float4*>(wmax + 4);
       am = fmaxf(fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)), fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w)));
-      gs = group_scale(am * rs, p.scale_type);
+      gs = group_scale<FAST>(am * rs, p.scale_type);
       if (t == 0) store_scale(p.scales, row, gs, p.scale_type);
     }
     const int per = p.group >> 3;  // vectors per group
@@ -240,6 +248,7 @@ __device__ __forceinline__ void finish_row(const P& p, float ss, const float (&z
     constexpr int B = KMAX <= 4 ? KMAX : 2;
 #pragma unroll
     for (int j0 = 0; j0 < KMAX; j0 += B) {
+      if (!EXACT && j0 * threads >= vpr) break;
       float y[B][8], a[B];
 #pragma unroll
       for (int u = 0; u < B; ++u) {
@@ -247,8 +256,7 @@ __device__ __forceinline__ void finish_row(const P& p, float ss, const float (&z
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[u][i] = 0.0f;
         if (EXACT || v < vpr) {
-          if constexpr (GN == KMAX) scale8(z[j], rs, g_reg[j], y[u]);
-          else scale8(z[j], rs, __ldg(p.gamma + v), y[u]);
+          scale8(z[j], rs, gamma(j, v), y[u]);
         }
         a[u] = amax8(y[u]);
       }
@@ -262,7 +270,7 @@ __device__ __forceinline__ void finish_row(const P& p, float ss, const float (&z
         const int v = (j0 + u) * threads + t;
         if (EXACT || v < vpr) {
           if (!row_scale) {
-            gs = group_scale(a[u], p.scale_type);
+            gs = group_scale<FAST>(a[u], p.scale_type);
             if ((v & (per - 1)) == 0)
               store_scale(p.scales, (row * vpr + v) / per, gs, p.scale_type);
           }
@@ -279,8 +287,7 @@ __device__ __forceinline__ void finish_row(const P& p, float ss, const float (&z
       const int v = j * threads + t;
       if (EXACT || v < vpr) {
         float y[8];
-        if constexpr (GN == KMAX) scale8(z[j], rs, g_reg[j], y);
-        else scale8(z[j], rs, __ldg(p.gamma + v), y);
+        scale8(z[j], rs, gamma(j, v), y);
         if (p.l2_stream) __stcs(out_row + v, pack8(y));
         else out_row[v] = pack8(y);
       }

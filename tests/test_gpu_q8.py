@@ -87,7 +87,8 @@ def test_q8_parity_odd_sizes(T, H, N, group):
 
 @pytest.mark.parametrize("T,H,N", [(1024, 8192, 8), (300, 8192, 4), (90, 8192, 12), (64, 32768, 2),
                                    (500, 1056, 3), (1300, 256, 1), (2000, 1056, 3), (700, 4096, 8),
-                                   (1300, 2816, 2), (700, 4992, 3), (400, 1024, 14)])
+                                   (1300, 2816, 2), (700, 4992, 3), (400, 1024, 14),
+                                   (320, 12000, 3), (200, 8704, 8), (170, 16352, 12)])
 @pytest.mark.parametrize("group,kind", [(0, "f32"), (32, "e8m0")])
 def test_q8_is_bitwise_the_same_under_every_budget_and_shard(T, H, N, group, kind):
     p, r, g = synth.make_inputs(T, H, N, 0.1, seed=5)
