@@ -46,7 +46,8 @@ sys.path.insert(0, ROOT)
 METRIC = "fused reduce+RMSNorm GB/s and % of GB300 HBM peak; tokens/s at T=1K–16K"
 PLANNER_SMS = 148  # SMs the planner models for the compute kernels (split workload)
 FALLBACK_HBM_GBS = 6800.0
-KERNEL_SRC = os.path.join(ROOT, "reduce_rmsnorm_gb300", "csrc", "fused_forms.cuh")
+KERNEL_SRC = [os.path.join(ROOT, "reduce_rmsnorm_gb300", "csrc", name)
+              for name in ("fused_forms.cuh", "ring_ops.cuh", "row_ops.cuh")]
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "fused_kernel_traffic.json")
 
 
@@ -67,8 +68,10 @@ def kernel_sha(path=None):
     """Fingerprint of the kernel's code: its source with comments removed and
     whitespace runs collapsed, so that editing prose keeps the ncu record
     while any change to the code orphans it."""
-    with open(path or KERNEL_SRC) as f:
-        src = f.read()
+    src = ""
+    for name in [path] if path else KERNEL_SRC:
+        with open(name) as f:
+            src += f.read()
     src = re.sub(r"/\*.*?\*/", " ", src, flags=re.S)
     src = re.sub(r"//[^\n]*", " ", src)
     return hashlib.sha256(" ".join(src.split()).encode()).hexdigest()[:16]

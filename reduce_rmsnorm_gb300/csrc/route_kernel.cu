@@ -48,11 +48,13 @@ constexpr int kRouteBlocks = 152 * 12;  // about what is resident at once; large
 // 8192, 17.9 / 19.6 at 16384, 27.1 / 33.6 at 32768.
 constexpr int64_t kLongTokens = 4096;
 constexpr int64_t kLongTokensByValue = 12288;
-// Resident blocks per SM that the 32 fp32 values of a lane leave registers for
-// (168 registers, three blocks, without a bound: 256 experts, sigmoid + bias +
-// groups 18.8 against 17.9 us at 16384 tokens, 29.6 / 27.1 at 32768; a bound
-// for the others made them slower).
-constexpr int kBlocks32 = 5;
+// Resident blocks per SM that several rows per warp leave registers for: the
+// 32 fp32 values of a lane (168 registers, three blocks, without a bound: 256
+// experts, sigmoid + bias + groups 18.8 against 17.9 us at 16384 tokens, 29.6 /
+// 27.1 at 32768), and 8 values (108 registers; 64 experts, bf16 8.1 against 7.3
+// us at 32768). The other lengths are left to the compiler (0): a bound made
+// them slower.
+constexpr int kBlocks32 = 5, kBlocks8 = 8;
 constexpr unsigned kAll = 0xffffffffu;
 constexpr uint32_t kNone = 1024u;          // fixed-point keys below: no candidate
 constexpr uint32_t kNone16 = 0x00800000u;  // the same for keys of bf16 logits
@@ -918,17 +920,20 @@ __device__ __noinline__ void route_again(const RouteParams& p, long long row, in
 // ------------------------------------------------------------------ several rows per warp
 
 // The 8 largest keys of a row in every one of its L lanes, descending, from
-// the lanes' 8 largest; next: the largest key that is not among them.
+// the lanes' 8 largest; next (if wanted): the largest key that is not among
+// them.
 template <int L>
-__device__ __forceinline__ void merge_lanes(uint32_t (&k)[8], uint32_t& next) {
+__device__ __forceinline__ void merge_lanes(uint32_t (&k)[8], uint32_t& next, bool wanted) {
 #pragma unroll
   for (int o = 1; o < L; o <<= 1) {
     uint32_t b[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) b[i] = __shfl_xor_sync(kAll, k[i], o);
+    if (wanted) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) next = max(next, min(k[i], b[7 - i]));
-    next = max(next, __shfl_xor_sync(kAll, next, o));
+      for (int i = 0; i < 8; ++i) next = max(next, min(k[i], b[7 - i]));
+      next = max(next, __shfl_xor_sync(kAll, next, o));
+    }
     merge8(k, b);
   }
 }
@@ -938,7 +943,7 @@ __device__ __forceinline__ void merge_lanes(uint32_t (&k)[8], uint32_t& next) {
 // instructions a level, for all rows of the warp at once); otherwise (V = 8)
 // K rounds of a maximum over the lanes' first keys.
 template <int V, int L, bool SMALLK, bool SIGMOID, bool BF16, bool VEC>
-__global__ void __launch_bounds__(kRouteWarps * 32, V == 32 && !BF16 ? kBlocks32 : 1)
+__global__ void __launch_bounds__(kRouteWarps * 32, V == 8 ? kBlocks8 : V == 32 && !BF16 ? kBlocks32 : 0)
     route_rows_kernel(const __grid_constant__ RouteParams p) {
   static_assert(V == 8 || SMALLK, "longer lists keep their 8 largest keys");
   constexpr int kRows = 32 / L;  // rows of a warp
@@ -1112,7 +1117,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, V == 32 && !BF16 ? kBlocks32
     int found = 0;
     bool near = false, open = false;
     if constexpr (SMALLK) {
-      merge_lanes<L>(k, next);
+      merge_lanes<L>(k, next, check || V > 8);  // a branch costs long lists more than it saves
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const bool is = i < p.k && k[i] >= none;
