@@ -241,7 +241,8 @@ __device__ __forceinline__ void finish_row(const P& p, float ss, const float (&z
       gs = group_scale<FAST>(am * rs, p.scale_type);
       if (t == 0) store_scale(p.scales, row, gs, p.scale_type);
     }
-    const int per = p.group >> 3;  // vectors per group
+    const int per = p.group >> 3;  // vectors per group, a power of two unless it is the row
+    const int per_log2 = 31 - __clz(per);
     // a few slots at a time, so that their shuffles overlap: T = 8192, H =
     // 16384, N = 8 takes 404 us with one slot at a time, 400 with two, 418 with
     // four
@@ -272,7 +273,7 @@ __device__ __forceinline__ void finish_row(const P& p, float ss, const float (&z
           if (!row_scale) {
             gs = group_scale<FAST>(a[u], p.scale_type);
             if ((v & (per - 1)) == 0)
-              store_scale(p.scales, (row * vpr + v) / per, gs, p.scale_type);
+              store_scale(p.scales, (row * vpr + v) >> per_log2, gs, p.scale_type);
           }
           const uint2 q = pack_e4m3(y[u], gs.inv);
           if (p.l2_stream) __stcs(out_row + v, q);
