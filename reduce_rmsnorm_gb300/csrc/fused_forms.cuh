@@ -735,7 +735,7 @@ int vpt_for(int n) { return n <= 8 ? 2 : 1; }
 //    T = 128-152 and within 3% at T <= 64; from one CUDA graph 11-23% faster,
 //    except at H = 8192, N = 8, T <= 64 (-3% to +4%). At H = 16384 (N = 2, 4,
 //    8) never slower per launch; back to back 9-22% faster at N = 2, 3-7% at
-//    N = 8, unchanged at N = 4. Ragged rows (H = 1024, 3072, 5120, 6144,
+//    N = 8, unchanged at N = 4. Ragged rows (H = 1024, 5120, 6144,
 //    7168, 12288; N = 2, 8; T = 32-152): never slower per launch, from one
 //    CUDA graph 5-30% faster, back to back mostly 5-17% faster.
 //  * otherwise the chunk ring with one pipeline.
